@@ -81,7 +81,10 @@ typedef enum {
   V4A_ERR_DEVICE_CHECK = 6
 } v4attn_status;
 
-typedef enum { V4A_F32 = 0, V4A_BF16 = 1, V4A_E4M3_BF16ROPE = 2, V4A_MXFP4 = 3 } v4attn_dtype;
+typedef enum {
+  V4A_F32 = 0, V4A_BF16 = 1, V4A_E4M3_BF16ROPE = 2, V4A_MXFP4 = 3,
+  V4A_F16 = 4            /* the 16-bit K/V layers only */
+} v4attn_dtype;
 
 typedef enum { V4A_CSA = 0, V4A_HCA = 1 } v4attn_kind;
 
@@ -312,6 +315,105 @@ v4attn_status v4attn_dense_mqa(const v4attn_layer_desc* desc, const v4attn_mqa_a
 v4attn_status v4attn_decode(const v4attn_layer_desc* desc, const v4attn_decode_args* args,
                             void* ws, size_t ws_bytes, cudaStream_t stream);
 v4attn_status v4attn_project(const v4attn_project_args* args, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- 16-bit K/V layers
+ * Layers whose history is kept uncompressed, as K and V rows of Hkv heads in
+ * bf16 or fp16: the grouped-query cache that the pages compare the compressed
+ * one with.  Its pools share the block tables of the compressed ones (blocks
+ * of 128 raw tokens): K and V are each [n_blocks][Hkv][128][d], and position p
+ * of sequence b is row p % 128 of block block_table[b][p / 128].
+ *
+ * Every call takes a ragged batch of new tokens: sequence b owns the token
+ * rows q_start[b] .. q_start[b+1]-1 (n_b of them, none allowed), which sit at
+ * the positions kv_len[b] - n_b .. kv_len[b] - 1; kv_len[b] counts the new
+ * tokens and may be 0.  One token a sequence is a decode step, a chunk a
+ * prefill; both may share a batch.  Token rows outside [q_start[0],
+ * q_start[B]) are left as they were in every output.
+ *
+ * Checked by the kernels (status bit, the access skipped): a q_start that
+ * decreases or leaves [0, T] (its sequence's rows are not taken); a position below 0 or past the block table (an
+ * append leaves its token out, a query below 0 sees no key); a table entry
+ * outside [0, n_blocks) (an append does not write, an attention does not see
+ * the block's keys).  Two tokens of one call must not fall on the same cache
+ * row (a block listed twice in the table): which one stays is not defined.
+ * Row strides are in elements and multiples of 8, every row's d values are
+ * contiguous, every pointer is 16-byte aligned (q_start and block_table 4,
+ * kv_len 8, lse and sink 4, idx 4), else V4A_ERR_INVALID_ARG.  The inputs, the
+ * caches and the outputs must not overlap one another (q_out may be q).
+ * blocks_per_seq <= 2^23, T <= 2^20, B <= 65535, Hq <= 1024. */
+typedef struct {
+  int32_t Hq, Hkv;            /* query and K/V heads: Hq % Hkv == 0, Hq / Hkv <= 128; query head
+                                 h reads K/V head h / (Hq / Hkv) */
+  int32_t d;                  /* head dim: 64 or 128 */
+  int32_t d_rope;             /* rotated dims at the end of d: a multiple of 16, 0 = none */
+  float rope_theta;           /* RoPE base */
+  int32_t rope_halves;        /* pairs: 0 adjacent (2k, 2k+1), 1 half of d_rope apart */
+  float softmax_scale;        /* <= 0 selects 1/sqrt(d) */
+  int32_t n_win;              /* paged_attention: keys a query sees, its own included; 0 = all */
+  int32_t dtype;              /* V4A_BF16 or V4A_F16: q, k, v, caches and outputs */
+} v4attn_kv_desc;
+
+/* Append the new tokens: k rotated to its position, v as it is, into their
+ * cache rows; optionally q rotated into q_out.  Angles p theta^(-2k/d_rope)
+ * are formed in double; products in fp32, rounded once. */
+typedef struct {
+  int32_t T, B;
+  const void* k; int64_t k_token_stride, k_head_stride;          /* [T][Hkv][d] */
+  const void* v; int64_t v_token_stride, v_head_stride;          /* [T][Hkv][d] */
+  const void* q; int64_t q_token_stride, q_head_stride;          /* [T][Hq][d] or NULL */
+  void* q_out; int64_t q_out_token_stride, q_out_head_stride;    /* with q; may be q itself */
+  void* k_cache; void* v_cache; int64_t n_blocks;
+  const int32_t* q_start;     /* device [B + 1] */
+  const int64_t* kv_len;      /* device [B], new tokens included */
+  const int32_t* block_table; /* device [B][blocks_per_seq] */
+  int32_t blocks_per_seq;
+} v4attn_kv_append_args;
+
+/* Attention of the new tokens over the cache (append them first): the query
+ * of head h at position p sees the keys j <= p of its sequence,
+ *   paged_attention:         with n_win > 0 only j > p - n_win;
+ *   block_sparse_attention:  only j whose block j / 128 is in the query's list
+ *     or among its last n_local blocks (p / 128 - n_local + 1 .. p / 128).  A
+ *     list's entry counts when it is >= 0, above every entry before it and
+ *     <= p / 128: ascending block ids, -1 behind them, as v4attn_index_topk
+ *     with m = 128 writes them.  The layer's n_win must be 0.
+ *   s_j = softmax_scale q . k_j,  den = exp(sink_h) + sum_j exp(s_j)
+ *   out = sum_j exp(s_j) v_j / den,  lse = log den
+ * A query that sees no key gets out = 0 and lse = sink_h (-inf without sinks).
+ * q . k, the softmax and its sums are fp32, exp(s_j) enters the product with
+ * v_j in the cache's type.  Rows past a sequence's kv_len, rows of blocks that
+ * no query of a call sees and rows before the first window may hold anything;
+ * a non-finite value in a row that some query of the call sees may reach the
+ * other queries of its sequence. */
+typedef struct {
+  int32_t T, B;
+  const void* q; int64_t q_token_stride, q_head_stride;          /* [T][Hq][d] */
+  const void* k_cache; const void* v_cache; int64_t n_blocks;
+  const int32_t* q_start;     /* device [B + 1] */
+  const int64_t* kv_len;      /* device [B] */
+  const int32_t* block_table; /* device [B][blocks_per_seq] */
+  int32_t blocks_per_seq;
+  const int32_t* idx;         /* block_sparse: device [T][n_lists][n_sel]; else NULL */
+  int32_t n_lists;            /* 1 (one list for every head) or Hkv */
+  int32_t n_sel;              /* 0 .. 4096; 0: only the last n_local blocks, idx may be NULL */
+  int32_t n_local;            /* >= 0 */
+  const float* sink;          /* device [Hq] or NULL */
+  void* out; int64_t out_token_stride, out_head_stride;          /* [T][Hq][d] */
+  float* lse;                 /* device [T][Hq] or NULL */
+} v4attn_kv_attn_args;
+
+/* Bytes of workspace for calls on this layer, of any size; 0 for a layer that
+ * is refused.  Zero its header with v4attn_workspace_init before the first
+ * call; one workspace serves one stream at a time (two captured graphs may
+ * share it when their replays are ordered). */
+size_t v4attn_kv_workspace_size(const v4attn_kv_desc* desc);
+v4attn_status v4attn_kv_append(const v4attn_kv_desc* desc, const v4attn_kv_append_args* args,
+                               void* ws, size_t ws_bytes, cudaStream_t stream);
+v4attn_status v4attn_paged_attention(const v4attn_kv_desc* desc, const v4attn_kv_attn_args* args,
+                                     void* ws, size_t ws_bytes, cudaStream_t stream);
+v4attn_status v4attn_block_sparse_attention(const v4attn_kv_desc* desc,
+                                            const v4attn_kv_attn_args* args, void* ws,
+                                            size_t ws_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------- no-allocation variant
  * The paper has no counterpart to this call; it is a convenience of this

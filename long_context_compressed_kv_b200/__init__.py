@@ -15,17 +15,18 @@ from typing import Optional
 import torch
 
 from . import _abi
-from ._abi import (BF16, CSA, E4M3_BF16ROPE, F32, HCA, MXFP4, CompressArgs, DecodeArgs,
-                   IndexArgs, LayerDesc, MqaArgs, ProjectArgs)
+from ._abi import (BF16, CSA, E4M3_BF16ROPE, F16, F32, HCA, MXFP4, CompressArgs, DecodeArgs,
+                   IndexArgs, KvAppendArgs, KvAttnArgs, KvDesc, LayerDesc, MqaArgs, ProjectArgs)
 
 _lib = _abi.load()
 
-__all__ = ["F32", "BF16", "E4M3_BF16ROPE", "MXFP4", "CSA", "HCA", "V4AttnError", "layer_desc",
+__all__ = ["F32", "BF16", "F16", "E4M3_BF16ROPE", "MXFP4", "CSA", "HCA", "V4AttnError", "layer_desc",
            "workspace", "workspace_size", "workspace_init", "compress", "index_topk",
            "index_topk_noalloc", "noalloc_device_status", "debug_index_stall",
            "device_status_code", "tc_peak_probe",
            "sparse_mqa", "dense_mqa",
-           "decode", "project", "device_status", "build_info", "row_bytes"]
+           "decode", "project", "device_status", "build_info", "row_bytes",
+           "kv_desc", "kv_workspace", "kv_append", "paged_attention", "block_sparse_attention"]
 
 
 class V4AttnError(RuntimeError):
@@ -239,6 +240,140 @@ def project(X, W, Y, stream=None):
     a = ProjectArgs(M, N, K, _p(X), _dt(X), X.stride(0), _p(W), _dt(W), W.stride(0), _p(Y), _dt(Y),
                     Y.stride(0))
     _check("v4attn_project", _lib.v4attn_project(ctypes.byref(a), _stream(stream)))
+
+
+# ---------------------------------------------------------------- 16-bit K/V layers
+_KV_DTYPES = {torch.bfloat16: BF16, torch.float16: F16}
+
+
+def kv_desc(Hq: int, Hkv: int, d: int, *, dtype=torch.bfloat16, d_rope: Optional[int] = None,
+            rope_theta: float = 160000.0, rope_halves: bool = False, softmax_scale: float = 0.0,
+            n_win: int = 0) -> KvDesc:
+    """An uncompressed layer: Hq query and Hkv K/V heads of d dims in ``dtype``
+    (bfloat16 or float16), d_rope of them rotated (default: all); see "16-bit
+    K/V layers" in include/v4attn.h."""
+    if dtype not in _KV_DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return KvDesc(Hq, Hkv, d, d if d_rope is None else d_rope, rope_theta, int(rope_halves),
+                  softmax_scale, n_win, _KV_DTYPES[dtype])
+
+
+def kv_workspace(desc: KvDesc, device="cuda") -> torch.Tensor:
+    """A zero-status workspace for the calls on this layer, whatever their size."""
+    n = _lib.v4attn_kv_workspace_size(ctypes.byref(desc))
+    if n == 0:
+        raise V4AttnError("v4attn_kv_workspace_size", _abi.ERR_INVALID_ARG)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        _check("v4attn_workspace_init", _lib.v4attn_workspace_init(_p(ws), ws.numel(), _stream()))
+    return ws
+
+
+def _kv_rows(name, t, T, H, desc):
+    """(pointer, token stride, head stride) of [T][H][d] rows; their last dim contiguous."""
+    if t.dim() != 3 or tuple(t.shape) != (T, H, desc.d):
+        raise ValueError(f"{name} must be [{T}][{H}][{desc.d}], got {tuple(t.shape)}")
+    if _KV_DTYPES.get(t.dtype) != desc.dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, not the layer's")
+    if t.stride(2) != 1 and t.numel():
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    # a dimension of one element may have any stride: it is never taken
+    return (_p(t) if t.numel() else None, t.stride(0) if T > 1 else H * desc.d,
+            t.stride(1) if H > 1 else desc.d)
+
+
+def _kv_small(name, t, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    return _p(t)
+
+
+def _kv_common(desc, T, k_cache, v_cache, q_start, kv_len, block_table, ws, others):
+    """Checked (B, pool and table fields) of a call on a 16-bit K/V layer."""
+    for t in (k_cache, v_cache, q_start, kv_len, block_table, ws, *others):
+        if t is not None and t.device != k_cache.device:
+            raise ValueError(f"tensors on {t.device} and {k_cache.device} in one call")
+    B = int(kv_len.numel())
+    pool = (int(k_cache.shape[0]), desc.Hkv, 128, desc.d)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if _KV_DTYPES.get(t.dtype) != desc.dtype or tuple(t.shape) != pool or \
+                not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {pool} tensor of the layer's dtype, got "
+                             f"{t.dtype} {tuple(t.shape)}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B][blocks_per_seq]")
+    bps = int(block_table.shape[1])
+    return B, (_p(k_cache), _p(v_cache), pool[0],
+               _kv_small("q_start", q_start, torch.int32, (B + 1,)),
+               _kv_small("kv_len", kv_len, torch.int64, (B,)),
+               _kv_small("block_table", block_table, torch.int32, (B, bps)), bps)
+
+
+def _kv_call(fn, desc, a, ws, device, stream):
+    # on the tensors' device, whichever is current
+    with torch.cuda.device(device):
+        _check(fn, getattr(_lib, fn)(ctypes.byref(desc), ctypes.byref(a), _p(ws), ws.numel(),
+                                     _stream(stream)))
+
+
+def kv_append(desc: KvDesc, *, k, v, k_cache, v_cache, q_start, kv_len, block_table, ws, q=None,
+              q_out=None, stream=None):
+    """Append new tokens to a paged K/V cache, K rotated to its position; with
+    ``q`` also the queries, rotated into ``q_out`` (which may be ``q``).
+
+    k, v [T][Hkv][d], q [T][Hq][d] (strided views allowed); k_cache, v_cache
+    [n_blocks][Hkv][128][d]; q_start int32 [B + 1], kv_len int64 [B] (new tokens
+    included), block_table int32 [B][blocks_per_seq]."""
+    T = int(k.shape[0])
+    B, cache = _kv_common(desc, T, k_cache, v_cache, q_start, kv_len, block_table, ws,
+                          (k, v, q, q_out))
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    none = (None, 0, 0)
+    a = KvAppendArgs(T, B, *_kv_rows("k", k, T, desc.Hkv, desc),
+                     *_kv_rows("v", v, T, desc.Hkv, desc),
+                     *(none if q is None else _kv_rows("q", q, T, desc.Hq, desc)),
+                     *(none if q is None else _kv_rows("q_out", q_out, T, desc.Hq, desc)), *cache)
+    _kv_call("v4attn_kv_append", desc, a, ws, k_cache.device, stream)
+
+
+def _kv_attention(fn, desc, q, k_cache, v_cache, q_start, kv_len, block_table, out, ws, lse, sink,
+                  idx, n_local, stream):
+    T = int(q.shape[0])
+    B, cache = _kv_common(desc, T, k_cache, v_cache, q_start, kv_len, block_table, ws,
+                          (q, out, lse, sink, idx))
+    lists = (None, 1, 0)
+    if idx is not None:
+        if idx.dim() == 2:
+            idx = idx[:, None]
+        if idx.dim() != 3:
+            raise ValueError("idx must be [T][n_lists][n_sel] or [T][n_sel]")
+        lists = (_kv_small("idx", idx, torch.int32, (T, *idx.shape[1:])), *idx.shape[1:])
+    a = KvAttnArgs(T, B, *_kv_rows("q", q, T, desc.Hq, desc), *cache, *lists, n_local,
+                   None if sink is None else _kv_small("sink", sink, torch.float32, (desc.Hq,)),
+                   *_kv_rows("out", out, T, desc.Hq, desc),
+                   None if lse is None else _kv_small("lse", lse, torch.float32, (T, desc.Hq)))
+    _kv_call(fn, desc, a, ws, k_cache.device, stream)
+
+
+def paged_attention(desc: KvDesc, *, q, k_cache, v_cache, q_start, kv_len, block_table, out, ws,
+                    lse=None, sink=None, stream=None):
+    """Attention of new tokens (decode steps, prefill chunks, or both in one
+    batch) over a paged K/V cache; arguments as ``kv_append``, q and out
+    [T][Hq][d], lse float32 [T][Hq], sink float32 [Hq]."""
+    _kv_attention("v4attn_paged_attention", desc, q, k_cache, v_cache, q_start, kv_len,
+                  block_table, out, ws, lse, sink, None, 0, stream)
+
+
+def block_sparse_attention(desc: KvDesc, *, q, k_cache, v_cache, q_start, kv_len, block_table,
+                           idx, n_local: int, out, ws, lse=None, sink=None, stream=None):
+    """``paged_attention`` over the 128-token blocks selected for each query
+    (idx int32 [T][n_lists][n_sel] or [T][n_sel]: ascending block ids, -1 behind
+    them, e.g. from ``index_topk`` with m = 128; n_lists 1 or Hkv) and its last
+    n_local blocks."""
+    _kv_attention("v4attn_block_sparse_attention", desc, q, k_cache, v_cache, q_start, kv_len,
+                  block_table, out, ws, lse, sink, idx, n_local, stream)
 
 
 def device_status(ws, stream=None) -> int:

@@ -10,7 +10,7 @@ LIB_PATH = os.path.join(HERE, "libv4attn.so")
 # status codes
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE_CHECK = range(7)
 # dtypes
-F32, BF16, E4M3_BF16ROPE, MXFP4 = range(4)
+F32, BF16, E4M3_BF16ROPE, MXFP4, F16 = range(5)
 NOALLOC_MAX_SCORES = 2097152   # V4A_NOALLOC_MAX_SCORES
 NOALLOC_MAX_QUERIES = 1365     # V4A_NOALLOC_MAX_QUERIES
 # layer kinds
@@ -71,9 +71,38 @@ class ProjectArgs(ctypes.Structure):
                 ("y_dtype", c_i32), ("ldy", c_i64)]
 
 
+class KvDesc(ctypes.Structure):
+    _fields_ = [("Hq", c_i32), ("Hkv", c_i32), ("d", c_i32), ("d_rope", c_i32),
+                ("rope_theta", c_f32), ("rope_halves", c_i32), ("softmax_scale", c_f32),
+                ("n_win", c_i32), ("dtype", c_i32)]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [("T", c_i32), ("B", c_i32),
+                ("k", c_ptr), ("k_token_stride", c_i64), ("k_head_stride", c_i64),
+                ("v", c_ptr), ("v_token_stride", c_i64), ("v_head_stride", c_i64),
+                ("q", c_ptr), ("q_token_stride", c_i64), ("q_head_stride", c_i64),
+                ("q_out", c_ptr), ("q_out_token_stride", c_i64), ("q_out_head_stride", c_i64),
+                ("k_cache", c_ptr), ("v_cache", c_ptr), ("n_blocks", c_i64), ("q_start", c_ptr),
+                ("kv_len", c_ptr), ("block_table", c_ptr), ("blocks_per_seq", c_i32)]
+
+
+class KvAttnArgs(ctypes.Structure):
+    _fields_ = [("T", c_i32), ("B", c_i32),
+                ("q", c_ptr), ("q_token_stride", c_i64), ("q_head_stride", c_i64),
+                ("k_cache", c_ptr), ("v_cache", c_ptr), ("n_blocks", c_i64), ("q_start", c_ptr),
+                ("kv_len", c_ptr), ("block_table", c_ptr), ("blocks_per_seq", c_i32),
+                ("idx", c_ptr), ("n_lists", c_i32), ("n_sel", c_i32), ("n_local", c_i32),
+                ("sink", c_ptr),
+                ("out", c_ptr), ("out_token_stride", c_i64), ("out_head_stride", c_i64),
+                ("lse", c_ptr)]
+
+
 STRUCTS = {"v4attn_layer_desc": LayerDesc, "v4attn_compress_args": CompressArgs,
            "v4attn_index_args": IndexArgs, "v4attn_mqa_args": MqaArgs,
-           "v4attn_decode_args": DecodeArgs, "v4attn_project_args": ProjectArgs}
+           "v4attn_decode_args": DecodeArgs, "v4attn_project_args": ProjectArgs,
+           "v4attn_kv_desc": KvDesc, "v4attn_kv_append_args": KvAppendArgs,
+           "v4attn_kv_attn_args": KvAttnArgs}
 
 # entry point -> (restype, argtypes)
 SIGNATURES = {
@@ -90,6 +119,14 @@ SIGNATURES = {
     "v4attn_decode": (ctypes.c_int, [ctypes.POINTER(LayerDesc), ctypes.POINTER(DecodeArgs),
                                      c_ptr, c_sz, c_ptr]),
     "v4attn_project": (ctypes.c_int, [ctypes.POINTER(ProjectArgs), c_ptr]),
+    "v4attn_kv_workspace_size": (c_sz, [ctypes.POINTER(KvDesc)]),
+    "v4attn_kv_append": (ctypes.c_int, [ctypes.POINTER(KvDesc), ctypes.POINTER(KvAppendArgs),
+                                        c_ptr, c_sz, c_ptr]),
+    "v4attn_paged_attention": (ctypes.c_int, [ctypes.POINTER(KvDesc), ctypes.POINTER(KvAttnArgs),
+                                              c_ptr, c_sz, c_ptr]),
+    "v4attn_block_sparse_attention": (ctypes.c_int, [ctypes.POINTER(KvDesc),
+                                                     ctypes.POINTER(KvAttnArgs), c_ptr, c_sz,
+                                                     c_ptr]),
     "v4attn_index_topk_noalloc": (ctypes.c_int, [ctypes.POINTER(LayerDesc),
                                                  ctypes.POINTER(IndexArgs), c_ptr]),
     "v4attn_noalloc_device_status": (ctypes.c_int, [c_ptr, ctypes.POINTER(ctypes.c_uint32)]),

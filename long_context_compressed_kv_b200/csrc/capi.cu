@@ -97,11 +97,16 @@ float softmax_scale(const v4attn_layer_desc* d) {
 
 // the last CUDA error an entry point met on this host thread (v4attn_last_cuda_error)
 thread_local cudaError_t t_last_cuda = cudaSuccess;
-v4attn_status cuda_status(cudaError_t e) {
+
+}  // namespace
+
+v4attn_status v4a::cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return V4A_OK;
   t_last_cuda = e;
   return V4A_ERR_CUDA;
 }
+
+namespace {
 
 v4attn_status run_compress(const v4attn_layer_desc* d, const v4attn_compress_args* a,
                            cudaStream_t st) {

@@ -1,0 +1,54 @@
+// Kernel parameter blocks and launchers of the 16-bit K/V layers (internal).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace v4a {
+
+constexpr int kKvBlock = 128;       // positions a pool block holds
+
+// A ragged batch of new tokens over paged caches (see "16-bit K/V layers" in
+// v4attn.h).
+struct KvBatch {
+  int T, B;
+  const int32_t* q_start;
+  const int64_t* kv_len;
+  const int32_t* bt;
+  int bps;
+  int64_t n_blocks;
+  uint32_t* status;
+};
+
+// rows [T][H][d] of a 16-bit type, strides in elements
+struct KvRows {
+  const void* p = nullptr;
+  int64_t tok = 0, head = 0;
+};
+
+struct KvAppendParams {
+  KvBatch b;
+  int Hq, Hkv, d, d_rope, halves, f16;
+  KvRows q, k, v, q_out;              // q.p null: no queries
+  void *k_cache, *v_cache;
+  double freq[64];                    // theta^(-2k/d_rope) / (2 pi): turns per position
+};
+
+struct KvAttnParams {
+  KvBatch b;
+  int Hq, Hkv, g, d, f16;             // g = Hq / Hkv
+  float scale;
+  int n_win;                          // 0: no window
+  KvRows q, out;                      // out: written
+  const void *k_cache, *v_cache;
+  int sparse;                         // block lists and n_local instead of the window
+  const int32_t* idx;
+  int n_lists, n_sel, n_local;
+  const float* sink;
+  float* lse;
+};
+
+cudaError_t launch_kv_append(const KvAppendParams& P, cudaStream_t st);
+cudaError_t launch_kv_attn(const KvAttnParams& P, cudaStream_t st);
+
+}  // namespace v4a

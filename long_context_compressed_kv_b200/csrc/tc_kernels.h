@@ -17,6 +17,8 @@ cudaError_t index_scores_dispatch(const IndexParams& P, cudaStream_t st);
 cudaError_t mqa_dispatch(const MqaParams& P, cudaStream_t st);
 cudaError_t project_dispatch(const ProjectParams& P, cudaStream_t st);
 const char* build_info_string();
+// V4A_OK, or V4A_ERR_CUDA with the error kept for v4attn_last_cuda_error
+v4attn_status cuda_status(cudaError_t e);
 
 // 0: the tensor-core kernel takes these arguments; 1: a pointer is not
 // 16-byte aligned; 2: a shape or format the kernel does not cover.
