@@ -395,15 +395,16 @@ typedef struct {
   int32_t blocks_per_seq;
   const int32_t* idx;         /* block_sparse: device [T][n_lists][n_sel]; else NULL */
   int32_t n_lists;            /* 1 (one list for every head) or Hkv */
-  int32_t n_sel;              /* 0 .. 4096; 0: only the last n_local blocks, idx may be NULL */
+  int32_t n_sel;              /* 0 .. 2048; 0: only the last n_local blocks, idx may be NULL */
   int32_t n_local;            /* >= 0 */
   const float* sink;          /* device [Hq] or NULL */
   void* out; int64_t out_token_stride, out_head_stride;          /* [T][Hq][d] */
   float* lse;                 /* device [T][Hq] or NULL */
 } v4attn_kv_attn_args;
 
-/* Bytes of workspace for calls on this layer, of any size; 0 for a layer that
- * is refused.  Zero its header with v4attn_workspace_init before the first
+/* Bytes of workspace for calls on this layer, of any size (43 MB at d = 128, for
+ * the parts of queries whose keys are split over SMs); 0 for a layer that is
+ * refused.  Zero its header with v4attn_workspace_init before the first
  * call; one workspace serves one stream at a time (two captured graphs may
  * share it when their replays are ordered). */
 size_t v4attn_kv_workspace_size(const v4attn_kv_desc* desc);

@@ -9,6 +9,12 @@ using namespace v4a;
 
 namespace {
 
+// Workspace: [status header | parts | their statistics | their outputs]
+constexpr size_t kPartsOff = sizeof(WsHeader);
+constexpr size_t kMlOff = kPartsOff + sizeof(KvPart) * 2 * kKvMaxCtas;
+constexpr size_t kOutOff = kMlOff + sizeof(float2) * 2 * kKvMaxCtas * kKvPartRows;
+static_assert(kMlOff % 16 == 0 && kOutOff % 16 == 0, "workspace alignment");
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 v4attn_status check_kv_desc(const v4attn_kv_desc* d) {
@@ -42,7 +48,7 @@ v4attn_status check_batch(const v4attn_kv_desc* d, const Args* a, const void* ws
     return V4A_ERR_INVALID_ARG;
   if (a->n_blocks < 1 || a->blocks_per_seq < 1) return V4A_ERR_INVALID_ARG;
   // positions and the pools' row numbers are 32-bit
-  if (a->blocks_per_seq > (1 << 23) || a->n_blocks * d->Hkv * kKvBlock > (1ll << 31) - 1)
+  if (a->blocks_per_seq > (1 << 23) || a->n_blocks > kKvMaxRows / ((int64_t)d->Hkv * kKvBlock))
     return V4A_ERR_UNSUPPORTED;
   if (!ws || !aligned(ws, 16) || ws_bytes < v4attn_kv_workspace_size(d)) return V4A_ERR_WORKSPACE;
   return V4A_OK;
@@ -82,7 +88,7 @@ v4attn_status run_attention(const v4attn_kv_desc* d, const v4attn_kv_attn_args* 
   if (!aligned(a->sink, 4) || !aligned(a->lse, 4) || !aligned(a->idx, 4)) return V4A_ERR_INVALID_ARG;
   if (sparse) {
     if (d->n_win != 0 || a->n_local < 0 || a->n_sel < 0) return V4A_ERR_INVALID_ARG;
-    if (a->n_sel > 4096) return V4A_ERR_UNSUPPORTED;
+    if (a->n_sel > kKvMaxSel) return V4A_ERR_UNSUPPORTED;
     if (a->n_sel > 0 && (!a->idx || (a->n_lists != 1 && a->n_lists != d->Hkv)))
       return V4A_ERR_INVALID_ARG;
   }
@@ -94,7 +100,7 @@ v4attn_status run_attention(const v4attn_kv_desc* d, const v4attn_kv_attn_args* 
   P.d = d->d;
   P.f16 = d->dtype == V4A_F16;
   P.scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / sqrtf((float)d->d);
-  P.n_win = sparse ? 0 : d->n_win;
+  P.n_win = sparse || d->n_win >= (1 << 30) ? 0 : d->n_win;   // positions stay below 2^30
   P.q = rows(a->q, a->q_token_stride, a->q_head_stride);
   P.out = rows(a->out, a->out_token_stride, a->out_head_stride);
   P.k_cache = a->k_cache;
@@ -106,6 +112,10 @@ v4attn_status run_attention(const v4attn_kv_desc* d, const v4attn_kv_attn_args* 
   P.n_local = sparse ? a->n_local : 0;
   P.sink = a->sink;
   P.lse = a->lse;
+  uint8_t* w8 = reinterpret_cast<uint8_t*>(ws);
+  P.parts = reinterpret_cast<KvPart*>(w8 + kPartsOff);
+  P.part_ml = reinterpret_cast<float2*>(w8 + kMlOff);
+  P.part_o = reinterpret_cast<float*>(w8 + kOutOff);
   return cuda_status(launch_kv_attn(P, st));
 }
 
@@ -114,7 +124,8 @@ v4attn_status run_attention(const v4attn_kv_desc* d, const v4attn_kv_attn_args* 
 extern "C" {
 
 size_t v4attn_kv_workspace_size(const v4attn_kv_desc* desc) {
-  return check_kv_desc(desc) == V4A_OK ? sizeof(WsHeader) : 0;
+  if (check_kv_desc(desc) != V4A_OK) return 0;
+  return kOutOff + sizeof(float) * 2 * kKvMaxCtas * kKvPartRows * desc->d;
 }
 
 v4attn_status v4attn_kv_append(const v4attn_kv_desc* desc, const v4attn_kv_append_args* a, void* ws,

@@ -1,114 +1,1092 @@
 // Attention over a paged 16-bit K/V cache ("16-bit K/V layers" in v4attn.h),
-// dense (causal, optional window) and over selected blocks.
+// dense (causal, optional window) and over selected blocks, for single tokens,
+// chunks and ragged mixes of both: one persistent tcgen05 kernel, and a merge
+// of the parts of queries whose keys were split over CTAs.
 //
-// One CTA per (token, query head); each of its warps takes every fourth key,
-// the lanes sharing a key's dims, with the running maximum and sum of a
-// softmax; the warps' parts meet in shared memory.
+// Mathematics: softmax(q K^T) V in one pass over the keys, 128 (a pool block)
+// at a time: S = Q K^T, running maximum m and sum l of each row,
+// P = exp2(s scale log2e - m), O = O 2^(m_old - m) + P V.  O is rescaled only
+// when m would grow by more than 2^8 (P stays below 2^8, within fp16).
+//
+// Rows.  The g = Hq / Hkv query heads that share a K/V head are rows of one
+// tile: row r is token r / g, head r % g, tt = 128 / g tokens a tile.  An item
+// is (sequence, K/V head, up to 2 tt tokens).  A CTA has two slots, each with
+// its own S / P and O in TMEM and its own softmax warpgroup:
+//   more than tt tokens (chunks): a slot a tile, both on the same key blocks,
+//     so a block is loaded once for 256 rows;
+//   else (decode steps): both slots hold the one tile, even and odd blocks,
+//     merged at the end.
+// The MMA thread issues P V of one slot and the next Q K^T of the same slot
+// while the other slot's warps work on their scores.
+//
+// Work split: the items' key blocks, laid end to end, are cut into equal
+// ranges, one a CTA, so ragged lengths and the causal triangle balance
+// whatever their mix (lengths are read on the device; the host knows only
+// T).  A CTA's first and last pieces may be parts of an item: their O, m and l
+// go to the workspace (at most two a CTA) and kv_merge_kernel joins them.
+//
+// Warps: 0-3 / 4-7 softmax of slot 0 / 1 (a thread a row, TMEM lane quarter =
+// warp % 4), 8 MMA issue, 9 work list and TMA loads, 10-11 idle (they complete the
+// third warpgroup, whose registers the softmax warpgroups take over).
 #include "common.cuh"
 #include "kv_kernels.h"
+#include "tc_common.cuh"
+#include "tc_kernels.h"
 
 namespace v4a {
 
 namespace {
-constexpr int kWarps = 4;
+
+constexpr int NK = kKvBlock;                   // keys a block
+constexpr int MROWS = 128;                     // rows a tile
+// Three warpgroups: 384 threads launched with 168 registers each (64512 of
+// the SM's 65536); the third gives up what the softmax warpgroups, which hold
+// a row's 128 scores, take: 2 x 208 + 88 = 3 x 168.
+constexpr int NTHREADS = 384;
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kWindow = 2048;                  // blocks whose selection is joined at a time
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.0f;                  // log2 of the growth that rescales O
+// cost of an item besides its blocks, in blocks (Q load, epilogue)
+constexpr int kItemCost = 1;
+// least cost of a CTA's range
+constexpr int kMinRange = 3;
+
+// What a piece (a range of an item's blocks) tells the MMA and softmax warps.
+struct Piece {
+  int n;             // blocks
+  int dual;          // two tiles (a slot each) or one
+  int first, last;   // of the item's blocks in this CTA's range
+  int part;          // -1: the whole item, rows go to the output; else the part to write
+  int b, h, tok0, ntok;   // sequence, K/V head, first token row, tokens
+  int pos0;          // position of the first token
+  int len;           // positions with keys
+  int end;           // no piece: the CTA is done
+};
+
+template <int D, bool SPARSE>
+struct Cfg {
+  static constexpr int kTile = MROWS * D * 2;           // bytes of a Q, K or V tile
+  // ring of K / V tiles: what 227 KB leave beside two Q tiles (and the lists)
+  static constexpr int kStages = D == 128 ? (SPARSE ? 4 : 5) : 10;
+};
+
+template <int D, bool SPARSE>
+struct Smem {
+  using C = Cfg<D, SPARSE>;
+  alignas(1024) uint8_t q[2][C::kTile];
+  alignas(1024) uint8_t kv[C::kStages][C::kTile];
+  uint64_t full[C::kStages], empty[C::kStages];
+  uint64_t qfull, qempty, sready[2], pready[2], pfull[2], pempty[2], o1ready, o1free, done;
+  int blk[C::kStages];             // logical block of a V stage, -1: not to be seen
+  uint32_t mask[C::kStages];       // its tokens (sparse)
+  Piece piece[2];
+  float m1[MROWS], l1[MROWS];      // slot 1's statistics for the merge in the CTA
+  uint32_t tmem_base;
+  uint32_t list_mask[SPARSE ? kWindow : 1];
+  int list_blk[SPARSE ? kWindow : 1];
+};
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// MMA whose A operand (P) is read from tensor memory: M = 128 rows at lanes
+// 0..127, two 16-bit elements of K a column
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float x, float y) {
+  if (F16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// log of the denominator 2^top l; the sink itself, bit for bit, of a row without keys
+__device__ __forceinline__ float log_sum(float top, float l, bool no_key, const float* sink, int h) {
+  if (no_key) return sink ? sink[h] : -INFINITY;
+  return (top + log2f(l)) * kLn2;
+}
+// Registers a thread of the calling warpgroup may use from here on.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kWarps) kv_attn_kernel(KvAttnParams P) {
-  constexpr int E = D / 32;
-  __shared__ float part[kWarps][D], ms[kWarps], ls[kWarps];
-  const int t = blockIdx.x, hq = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = hq / P.g;
-  int b = 0;
-  for (int i = 0; i < P.b.B; i += 32 * kWarps)
-    b += __syncthreads_count(i + tid < P.b.B && P.b.q_start[i + tid + 1] <= t);
-  if (b >= P.b.B) return;
+// ---------------------------------------------------------------- work list
+// Everything below is a function of the lengths alone, so every CTA finds its
+// own range without a word from the others.
+
+struct SeqInfo {
+  int q0, n;         // first token row, tokens (0 when its q_start is bad)
+  int base;          // position of the first token
+  int len;           // positions with keys: kv_len cut to the table
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const KvAttnParams& P, int b, bool report) {
+  SeqInfo s;
   const int q0 = P.b.q_start[b], q1 = P.b.q_start[b + 1];
-  if (t < q0 || q0 < 0 || q1 > P.b.T) {
-    if ((b > 0 || t >= q0) && tid == 0) flag(P.b.status, ST_BAD_SEQ);
-    return;
+  const int64_t len = P.b.kv_len[b], cap = (int64_t)P.b.bps * NK;
+  const bool bad = q0 < 0 || q1 < q0 || q1 > P.b.T;
+  s.q0 = q0;
+  s.n = bad ? 0 : q1 - q0;
+  s.len = (int)max((int64_t)0, min(len, cap));
+  // a kv_len out of range still gives a 32-bit position
+  s.base = (int)(max((int64_t)0, min(len, (int64_t)1 << 30)) - s.n);
+  if (report) {
+    if (bad) flag(P.b.status, ST_BAD_SEQ);
+    if (s.n > 0 && (len > cap || len < s.n)) flag(P.b.status, ST_BAD_POSITION);
   }
-  int64_t p = P.b.kv_len[b] - (q1 - q0) + (t - q0);
-  const int64_t cap = (int64_t)P.b.bps * kKvBlock;
-  if ((p < 0 || p >= cap) && tid == 0) flag(P.b.status, ST_BAD_POSITION);
-  p = min(p, cap - 1);
-  auto load = [](const void* base, int64_t i) {
-    return F16 ? __half2float(reinterpret_cast<const __half*>(base)[i])
-               : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[i]);
-  };
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) {
-    q[e] = load(P.q.p, t * P.q.tok + hq * P.q.head + lane + 32 * e) * P.scale;
-    o[e] = 0.f;
-  }
-  const int32_t* list = P.sparse && P.n_sel
-                            ? P.idx + ((int64_t)t * P.n_lists + (P.n_lists > 1 ? h : 0)) * P.n_sel
-                            : nullptr;
-  auto block = [&](int64_t lb) {       // the keys of logical block lb
-    const int32_t pb = P.b.bt[(int64_t)b * P.b.bps + lb];
-    if (pb < 0 || pb >= P.b.n_blocks) {
-      if (lane == 0) flag(P.b.status, ST_BAD_INDEX);
-      return;
-    }
-    for (int c = warp; c < kKvBlock; c += kWarps) {
-      const int64_t j = lb * kKvBlock + c;
-      if (j > p || (P.n_win && j <= p - P.n_win)) continue;
-      const int64_t at = (((int64_t)pb * P.Hkv + h) * kKvBlock + c) * D;
-      float s = 0.f;
-      for (int e = 0; e < E; ++e) s += q[e] * load(P.k_cache, at + lane + 32 * e);
-      s = warp_sum(s);
-      const float mn = fmaxf(m, s), a = expf(m - mn), w = expf(s - mn);
-      l = l * a + w;
-      for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * load(P.v_cache, at + lane + 32 * e);
-      m = mn;
-    }
-  };
-  const int64_t last = p < 0 ? -1 : p / kKvBlock;
-  if (!P.sparse) {
-    const int64_t first = P.n_win ? max((int64_t)0, p - P.n_win + 1) / kKvBlock : 0;
-    for (int64_t lb = first; lb <= last; ++lb) block(lb);
-  } else {
-    const int64_t local = max((int64_t)0, last - P.n_local + 1);
-    int32_t before = -1;
-    for (int i = 0; i < P.n_sel; ++i) {
-      const int32_t e = list[i];
-      if (e > before && e < local && e <= last) block(e);
-      before = max(before, e);
-    }
-    for (int64_t lb = local; lb <= last; ++lb) block(lb);
-  }
-  for (int e = 0; e < E; ++e) part[warp][lane + 32 * e] = o[e];
-  if (lane == 0) {
-    ms[warp] = m;
-    ls[warp] = l;
-  }
-  __syncthreads();
-  float mm = P.sink ? P.sink[hq] : -INFINITY;
-  for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ms[w]);
-  const float mz = mm == -INFINITY ? 0.f : mm;
-  float den = P.sink ? expf(P.sink[hq] - mz) : 0.f;
-  for (int w = 0; w < kWarps; ++w) den += ls[w] * expf(ms[w] - mz);
-  for (int i = tid; i < D; i += 32 * kWarps) {
-    float x = 0.f;
-    for (int w = 0; w < kWarps; ++w) x += part[w][i] * expf(ms[w] - mz);
-    x = den > 0.f || den != den ? x / den : 0.f;
-    uint16_t* out = reinterpret_cast<uint16_t*>(const_cast<void*>(P.out.p)) + t * P.out.tok +
-                    hq * P.out.head + i;
-    if (F16)
-      *reinterpret_cast<__half*>(out) = __float2half_rn(x);
-    else
-      *out = f32_to_bf16_bits(x);
-  }
-  if (tid == 0 && P.lse) P.lse[(int64_t)t * P.Hq + hq] = mz + logf(den);
+  return s;
 }
 
-cudaError_t launch_kv_attn(const KvAttnParams& P, cudaStream_t st) {
-  const dim3 grid(P.b.T, P.Hq);
-  if (P.d == 128 && P.f16) kv_attn_kernel<128, true><<<grid, 32 * kWarps, 0, st>>>(P);
-  else if (P.d == 128) kv_attn_kernel<128, false><<<grid, 32 * kWarps, 0, st>>>(P);
-  else if (P.f16) kv_attn_kernel<64, true><<<grid, 32 * kWarps, 0, st>>>(P);
-  else kv_attn_kernel<64, false><<<grid, 32 * kWarps, 0, st>>>(P);
+// Blocks of tokens i0 .. i1-1 of a sequence: first block and count.  Sparse
+// items of one token walk their list's entries instead (n_sel + n_local).
+struct Span {
+  int lo, n;
+};
+__device__ __forceinline__ bool by_list(const KvAttnParams& P, int ntok) {
+  return P.sparse && ntok == 1;
+}
+__device__ __forceinline__ Span item_span(const KvAttnParams& P, const SeqInfo& s, int i0, int i1) {
+  Span r;
+  const int last = min(s.base + i1 - 1, s.len - 1);
+  if (by_list(P, i1 - i0)) {
+    r.lo = 0;
+    r.n = last < 0 ? 0 : min(P.n_sel + min(P.n_local, 1 << 23), last / NK + 1 + P.n_sel);
+    return r;
+  }
+  const int hi = last < 0 ? 0 : last / NK + 1;
+  r.lo = P.n_win ? min(max(0, s.base + i0 - P.n_win + 1) / NK, hi) : 0;
+  r.n = hi - r.lo;
+  return r;
+}
+
+// Cost of all items of one head of a sequence, found by the whole warp.
+__device__ __forceinline__ int64_t head_cost(const KvAttnParams& P, const SeqInfo& s, int per_item,
+                                             int lane) {
+  const int items = (s.n + per_item - 1) / per_item;
+  int64_t sum = 0;
+  for (int k = lane; k < items; k += 32)
+    sum += item_span(P, s, k * per_item, min(s.n, (k + 1) * per_item)).n + kItemCost;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+__device__ __forceinline__ SeqInfo shfl_seq(const SeqInfo& s, int src) {
+  SeqInfo r;
+  r.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+  r.n = __shfl_sync(0xffffffffu, s.n, src);
+  r.base = __shfl_sync(0xffffffffu, s.base, src);
+  r.len = __shfl_sync(0xffffffffu, s.len, src);
+  return r;
+}
+
+// The warp's place in the laid-out work: walks (sequence, head, item).
+struct Walk {
+  int b0;            // sequences b0 .. b0+31, one a lane
+  SeqInfo mine;      // this lane's sequence
+  int64_t cost;      // of all heads of this lane's sequence
+  int per_item;
+
+  __device__ __forceinline__ void load(const KvAttnParams& P, int first, int lane, bool report) {
+    b0 = first;
+    mine = SeqInfo{0, 0, 0, 0};
+    if (b0 + lane < P.b.B) mine = seq_info(P, b0 + lane, report);
+    cost = 0;
+    if (mine.n > 0 && mine.n <= per_item) cost = item_span(P, mine, 0, mine.n).n + kItemCost;
+    unsigned many = __ballot_sync(0xffffffffu, mine.n > per_item);
+    while (many) {
+      const int src = __ffs(many) - 1;
+      many &= many - 1;
+      const int64_t c = head_cost(P, shfl_seq(mine, src), per_item, lane);
+      if (lane == src) cost = c;
+    }
+    cost *= P.Hkv;
+  }
+};
+
+// ---------------------------------------------------------------- kernel
+
+template <int D, bool F16, bool SPARSE>
+struct Kernel {
+  using S = Smem<D, SPARSE>;
+  using C = Cfg<D, SPARSE>;
+  static constexpr int NST = C::kStages;
+  static constexpr int TM_S = 0, TM_O = 2 * NK;          // TMEM columns: S0 S1 O0 O1
+  static constexpr int kCols = 512;
+
+  // -------------------------------------------------------------- loads
+  static __device__ void produce(const KvAttnParams& P, S& s, const CUtensorMap* tm_q,
+                                 const CUtensorMap* tm_k, const CUtensorMap* tm_v) {
+    const int lane = threadIdx.x & 31;
+    uint32_t* status = P.b.status;
+    const int tt = P.tt, per_item = 2 * tt;
+    Walk w;
+    w.per_item = per_item;
+    int64_t total = 0;
+    for (int b0 = 0; b0 < P.b.B; b0 += 32) {
+      w.load(P, b0, lane, blockIdx.x == 0);
+      int64_t c = w.cost;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      total += c;
+    }
+    int64_t range = (total + gridDim.x - 1) / gridDim.x;
+    if (range < kMinRange) range = kMinRange;
+    const int64_t x0 = range * blockIdx.x, x1 = min(total, x0 + range);
+    KvPart* rec = P.parts + 2 * blockIdx.x;
+    if (lane < 2) rec[lane] = KvPart{0, 0, 0, 0};
+    __syncwarp();
+
+    int pieces = 0, it = 0, items = 0;
+    bool ok = true;
+    // publish a piece (lane 0 writes it)
+    auto publish = [&](const Piece& pc) -> bool {
+      const int i = pieces & 1, u = pieces >> 1;
+      if (u >= 1 && !mbar_wait_warp(&s.pempty[i], (u - 1) & 1, status, 0)) return false;
+      if (lane == 0) {
+        s.piece[i] = pc;
+        mbar_arrive(&s.pfull[i]);
+      }
+      __syncwarp();
+      ++pieces;
+      return true;
+    };
+    // Q of the current item, one tile a slot (rows past the sequence's tokens are
+    // never stored), once the item before has read its own: asked for when two
+    // blocks of the item are on their way, or at its end
+    int q_tiles = 0, q_head = 0, q_tok = 0, ahead = 0;
+    auto load_q = [&]() -> bool {
+      if (q_tiles == 0) return true;
+      if (items >= 1 && !mbar_wait_warp(&s.qempty, (items - 1) & 1, status, 2)) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&s.qfull, q_tiles * D * 2 * P.g * tt);
+        for (int t = 0; t < q_tiles; ++t)
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(s.q[t] + c * (MROWS * 128), tm_q, &s.qfull, 64 * c, q_head, q_tok + t * tt);
+      }
+      __syncwarp();
+      ++items;
+      q_tiles = ahead = 0;
+      return true;
+    };
+    // one block's K and V tiles (pb < 0: rows outside the pool, which TMA fills with zeros)
+    auto load_block = [&](int h, int lb, int pb, uint32_t mask) -> bool {
+      const int row = pb < 0 ? kKvMaxRows : (pb * P.Hkv + h) * NK;
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j, ++it) {
+        const int st = it % NST, u = it / NST;
+        if (u >= 1 && !mbar_wait_warp(&s.empty[st], (u - 1) & 1, status, 1)) return false;
+        if (lane == 0) {
+          if (j == 1) {
+            s.blk[st] = pb < 0 ? -1 : lb;
+            s.mask[st] = mask;
+          }
+          mbar_arrive_expect_tx(&s.full[st], C::kTile);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_2d(s.kv[st] + c * (MROWS * 128), j ? tm_v : tm_k, &s.full[st], 64 * c, row);
+        }
+        __syncwarp();
+      }
+      return q_tiles == 0 || ++ahead < 2 || load_q();
+    };
+    // the pool block of logical block lb (lane-wise); -1 where the table holds none
+    auto page = [&](int b, int lb, bool want) -> int {
+      int pb = -1;
+      if (want) {
+        pb = __ldg(P.b.bt + (int64_t)b * P.b.bps + lb);
+        if (pb < 0 || pb >= P.b.n_blocks) {
+          pb = -1;
+          flag(status, ST_BAD_INDEX);
+        }
+      }
+      return pb;
+    };
+
+    // find the first item of the range
+    int64_t at = 0;                    // place of the current group of sequences
+    for (int b0 = 0; ok && b0 < P.b.B && at < x1; b0 += 32) {
+      if (P.b.B > 32) w.load(P, b0, lane, false);
+      int64_t c = w.cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += v;
+      }
+      const int64_t end = at + c, begin = end - w.cost;     // this lane's sequence
+      const int64_t group_end = __shfl_sync(0xffffffffu, end, 31);
+      unsigned todo = __ballot_sync(0xffffffffu, w.cost > 0 && begin < x1 && end > x0);
+      while (ok && todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const SeqInfo q = shfl_seq(w.mine, src);
+        const int64_t sb = __shfl_sync(0xffffffffu, begin, src);
+        const int64_t hc = __shfl_sync(0xffffffffu, w.cost, src) / P.Hkv;
+        const int nit = (q.n + per_item - 1) / per_item;
+        int h = x0 > sb ? (int)((x0 - sb) / hc) : 0;
+        int64_t hx = sb + h * hc;                            // place of head h's first item
+        int k = 0;
+        int64_t ix = hx;
+        // first item of this head that reaches past x0, 32 at a time
+        if (x0 > hx) {
+          for (;;) {
+            int cst = 0;
+            if (k + lane < nit)
+              cst = item_span(P, q, (k + lane) * per_item, min(q.n, (k + lane + 1) * per_item)).n +
+                    kItemCost;
+            int64_t pre = cst;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+              if (lane >= o) pre += v;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, cst > 0 && ix + pre > x0);
+            if (hit) {
+              const int l0 = __ffs(hit) - 1;
+              ix += __shfl_sync(0xffffffffu, pre - cst, l0);
+              k += l0;
+              break;
+            }
+            ix += __shfl_sync(0xffffffffu, pre, 31);
+            k += 32;
+            if (k >= nit) break;                             // (cannot happen: the head holds x0)
+          }
+        }
+        for (; ok && h < P.Hkv && ix < x1; ++h, k = 0) {
+          for (; ok && k < nit && ix < x1; ++k) {
+            const int i0 = k * per_item, i1 = min(q.n, i0 + per_item);
+            const Span sp = item_span(P, q, i0, i1);
+            const int64_t iend = ix + sp.n + kItemCost;
+            // this CTA's blocks of the item: the first kItemCost places carry none
+            const int c0 = (int)(max(x0, ix) - ix), c1 = (int)(min(x1, iend) - ix);
+            const int e0 = max(c0 - kItemCost, 0), e1 = max(c1 - kItemCost, 0);
+            Piece pc;
+            pc.dual = i1 - i0 > tt;
+            pc.b = w.b0 + src;
+            pc.h = h;
+            pc.tok0 = q.q0 + i0;
+            pc.ntok = i1 - i0;
+            pc.pos0 = q.base + i0;
+            pc.len = q.len;
+            pc.end = 0;
+            pc.part = c0 == 0 && ix + c1 == iend ? -1 : 2 * (int)blockIdx.x + (c0 == 0 ? 1 : 0);
+            if (pc.part >= 0 && lane == 0) {
+              KvPart r;
+              r.rows = pc.ntok * P.g;
+              r.ends = ix + c1 == iend;
+              r.h = h;
+              r.tok0 = pc.tok0;
+              rec[pc.part & 1] = r;
+            }
+            q_tiles = pc.dual + 1;
+            q_head = h * P.g;
+            q_tok = pc.tok0;
+            if (items == 0) ok = load_q();
+            if (!SPARSE) {
+              pc.first = pc.last = 1;
+              pc.n = e1 - e0;
+              ok = ok && publish(pc);
+              for (int e = e0; ok && e < e1; e += 32) {
+                const int pb = page(pc.b, sp.lo + e + lane, e + lane < e1);
+                const int m = min(32, e1 - e);
+                for (int i = 0; ok && i < m; ++i)
+                  ok = load_block(h, sp.lo + e + i, __shfl_sync(0xffffffffu, pb, i), 0xffffffffu);
+              }
+            } else {
+              ok = ok && sparse_piece(P, s, pc, e0, e1, lane, publish, load_block, page);
+            }
+            ok = ok && load_q();
+            ix = iend;
+          }
+          if (ix >= x1) break;
+        }
+      }
+      at = group_end;
+    }
+    if (ok) {
+      Piece pc{};
+      pc.end = 1;
+      publish(pc);
+    }
+    // no load may still be landing when the CTA exits
+    if (lane == 0) {
+      for (int k = 0; k < NST && k < it; ++k) {
+        const int i2 = it - 1 - k;
+        mbar_wait(&s.full[i2 % NST], (i2 / NST) & 1);      // time bound only
+      }
+      if (items > 0) mbar_wait(&s.qfull, (items - 1) & 1);
+    }
+  }
+
+  // Selected blocks of a piece.  One token: list entries e0 .. e1-1 (its list,
+  // then its last blocks).  More: the blocks e0 .. e1-1 that any of them
+  // selected, with a bit for each token that did, joined in shared memory
+  // kWindow blocks at a time.
+  template <class Pub, class Load, class Page>
+  static __device__ bool sparse_piece(const KvAttnParams& P, S& s, Piece pc, int e0, int e1, int lane,
+                                      Pub& publish, Load& load_block, Page& page) {
+    const int li = P.n_lists > 1 ? pc.h : 0;
+    auto list_of = [&](int tok) { return P.idx + ((int64_t)(pc.tok0 + tok) * P.n_lists + li) * P.n_sel; };
+    // the warp's 32 entries from i0 on; good: they count, before: largest entry before them
+    auto entries = [&](const int32_t* list, int i0, int last, int& before, bool& good) -> int {
+      const int e = i0 + lane < P.n_sel ? __ldg(list + i0 + lane) : -1;
+      int top = e;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, top, o);
+        if (lane >= o) top = max(top, v);
+      }
+      int prev = __shfl_up_sync(0xffffffffu, top, 1);
+      prev = lane == 0 ? before : max(prev, before);
+      good = e >= 0 && e > prev && e <= last;
+      before = max(before, __shfl_sync(0xffffffffu, top, 31));
+      return e;
+    };
+    bool ok = true, first = true;
+    if (by_list(P, pc.ntok)) {
+      const int p = min(pc.pos0, pc.len - 1), last = p < 0 ? -1 : p / NK;
+      const int local = max(0, last - P.n_local + 1);          // first of the last blocks
+      // the list's blocks in front of them (n_sel <= kWindow)
+      int n = 0, before = -1;
+      for (int i = 0; i < min(P.n_sel, e1); i += 32) {
+        bool good;
+        const int e = entries(list_of(0), i, last, before, good);
+        good = good && e < local && i + lane >= e0 && i + lane < e1;
+        const unsigned m = __ballot_sync(0xffffffffu, good);
+        if (good) s.list_blk[n + __popc(m & ((1u << lane) - 1))] = e;
+        n += __popc(m);
+      }
+      // then the last blocks, entries n_sel + i
+      const int l0 = max(e0 - P.n_sel, 0), l1 = min(e1 - P.n_sel, last - local + 1);
+      const int nl = max(0, l1 - l0);
+      __syncwarp();
+      pc.first = pc.last = 1;
+      pc.n = n + nl;
+      ok = publish(pc);
+      for (int e = 0; ok && e < pc.n; e += 32) {
+        int lb = 0;
+        if (e + lane < pc.n) lb = e + lane < n ? s.list_blk[e + lane] : local + l0 + e + lane - n;
+        const int pb = page(pc.b, lb, e + lane < pc.n);
+        const int m = min(32, pc.n - e);
+        for (int i = 0; ok && i < m; ++i)
+          ok = load_block(pc.h, __shfl_sync(0xffffffffu, lb, i), __shfl_sync(0xffffffffu, pb, i),
+                          0xffffffffu);
+      }
+      return ok;
+    }
+    int w0 = e0;
+    do {
+      const int w1 = min(e1, w0 + kWindow);
+      for (int i = lane; i < w1 - w0; i += 32) s.list_mask[i] = 0;
+      __syncwarp();
+      for (int t = 0; t < pc.ntok; ++t) {
+        const int p = min(pc.pos0 + t, pc.len - 1), last = p < 0 ? -1 : p / NK;
+        const int local = max(0, last - P.n_local + 1);
+        int before = -1;
+        for (int i = 0; i < P.n_sel; i += 32) {
+          bool good;
+          const int e = entries(list_of(t), i, last, before, good);
+          if (good && e >= w0 && e < w1) atomicOr(&s.list_mask[e - w0], 1u << t);
+        }
+        for (int e = max(local, w0) + lane; e <= last && e < w1; e += 32)
+          atomicOr(&s.list_mask[e - w0], 1u << t);
+      }
+      __syncwarp();
+      int n = 0;
+      for (int i = 0; i < w1 - w0; i += 32) {
+        const uint32_t mk = i + lane < w1 - w0 ? s.list_mask[i + lane] : 0;
+        const unsigned m = __ballot_sync(0xffffffffu, mk != 0);
+        __syncwarp();
+        const int to = n + __popc(m & ((1u << lane) - 1));     // <= i + lane: in place
+        if (mk) {
+          s.list_mask[to] = mk;
+          s.list_blk[to] = w0 + i + lane;
+        }
+        n += __popc(m);
+        __syncwarp();
+      }
+      pc.first = first;
+      pc.last = w1 == e1;
+      pc.n = n;
+      ok = publish(pc);
+      first = false;
+      for (int e = 0; ok && e < n; e += 32) {
+        const int lb = e + lane < n ? s.list_blk[e + lane] : 0;
+        const uint32_t mk = e + lane < n ? s.list_mask[e + lane] : 0;
+        const int pb = page(pc.b, lb, e + lane < n);
+        const int m = min(32, n - e);
+        for (int i = 0; ok && i < m; ++i)
+          ok = load_block(pc.h, __shfl_sync(0xffffffffu, lb, i), __shfl_sync(0xffffffffu, pb, i),
+                          __shfl_sync(0xffffffffu, mk, i));
+      }
+      w0 = w1;
+    } while (ok && w0 < e1);
+    return ok;
+  }
+
+  // -------------------------------------------------------------- MMA issue
+  static __device__ void issue(const KvAttnParams& P, S& s, uint32_t tmem) {
+    const int lane = threadIdx.x & 31;
+    uint32_t* status = P.b.status;
+    const uint64_t k_bits = smem_desc_bits(16, 1024, 2);             // K-major, 128B swizzle
+    const uint64_t v_bits = smem_desc_bits(MROWS * 128, 1024, 2);    // MN-major, 128B swizzle
+    const uint32_t fmt = F16 ? 0 : 1;
+    const uint32_t id_qk = idesc_f(fmt, fmt, MROWS, NK, false, false);
+    const uint32_t id_pv = idesc_f(fmt, fmt, MROWS, D, false, true);
+    int base = 0, items = 0, np[2] = {0, 0};
+    uint32_t acc[2] = {0, 0};
+    auto wait_tile = [&](int i) { return mbar_wait_warp(&s.full[i % NST], (i / NST) & 1, status, 3); };
+    auto qk = [&](int slot, int qslot, int tile) {
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t a = smem_desc(s.q[qslot], k_bits), b = smem_desc(s.kv[tile % NST], k_bits);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          // 64 dims (4 steps of 32 bytes) a swizzled half of 128 rows x 128 bytes
+          const uint32_t off = (kk / 4) * (MROWS * 128 / 16) + (kk % 4) * 2;
+          mma_f16(tmem + TM_S + slot * NK, a + off, b + off, id_qk, kk > 0);
+        }
+      }
+    };
+    auto pv = [&](int slot, int tile) {
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t b = smem_desc(s.kv[tile % NST], v_bits);
+#pragma unroll
+        for (int kk = 0; kk < NK / 16; ++kk)      // 16 keys: 8 columns of P, 16 rows x 128 bytes
+          mma_f16_ts(tmem + TM_O + slot * D, tmem + TM_S + slot * NK + 8 * kk, b + 128 * kk, id_pv,
+                     kk > 0 ? 1u : acc[slot]);
+      }
+      acc[slot] = 1;
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (lane == 0) tc_commit(bar);
+    };
+    bool ok = true;
+    for (int pieces = 0; ok; ++pieces) {
+      const int pi = pieces & 1;
+      if (!mbar_wait_warp(&s.pfull[pi], (pieces >> 1) & 1, status, 4)) break;
+      const int n = s.piece[pi].n, dual = s.piece[pi].dual, first = s.piece[pi].first,
+                last = s.piece[pi].last, end = s.piece[pi].end;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.pempty[pi]);
+      if (end) break;
+      if (first) {
+        acc[0] = acc[1] = 0;
+        if (!mbar_wait_warp(&s.qfull, items & 1, status, 5)) break;
+        ++items;
+      }
+      auto wait_p = [&](int slot) {
+        const bool r = mbar_wait_warp(&s.pready[slot], np[slot] & 1, status, 6);
+        ++np[slot];
+        return r;
+      };
+      // block i's K at tile base + 2 i, its V at base + 2 i + 1
+      if (dual) {
+        if (n > 0) {
+          if (!(ok = wait_tile(base))) break;
+          qk(0, 0, base);
+          commit(&s.sready[0]);
+          qk(1, 1, base);
+          commit(&s.sready[1]);
+          commit(&s.empty[base % NST]);
+        }
+        for (int i = 0; ok && i < n; ++i) {
+          const int vt = base + 2 * i + 1, kt = vt + 1;
+          for (int slot = 0; slot < 2; ++slot) {
+            if (!(ok = wait_p(slot))) break;
+            if (slot == 0 && !(ok = wait_tile(vt))) break;
+            pv(slot, vt);
+            if (i + 1 < n) {
+              if (slot == 0 && !(ok = wait_tile(kt))) break;
+              if (slot == 1) commit(&s.empty[vt % NST]);
+              qk(slot, slot, kt);
+            }
+            commit(&s.sready[slot]);
+          }
+          if (!ok) break;
+          if (i + 1 < n)
+            commit(&s.empty[kt % NST]);
+          else
+            commit(&s.empty[vt % NST]);
+        }
+      } else {
+        for (int i = 0; ok && i < n && i < 2; ++i) {
+          if (!(ok = wait_tile(base + 2 * i))) break;
+          qk(i, 0, base + 2 * i);
+          commit(&s.sready[i]);
+          commit(&s.empty[(base + 2 * i) % NST]);
+        }
+        for (int i = 0; ok && i < n; ++i) {
+          const int slot = i & 1, vt = base + 2 * i + 1, kt = base + 2 * (i + 2);
+          if (!(ok = wait_p(slot)) || !(ok = wait_tile(vt))) break;
+          pv(slot, vt);
+          commit(&s.empty[vt % NST]);
+          if (i + 2 < n) {
+            if (!(ok = wait_tile(kt))) break;
+            qk(slot, 0, kt);
+            commit(&s.empty[kt % NST]);
+          }
+          commit(&s.sready[slot]);
+        }
+      }
+      if (!ok) break;
+      if (last) commit(&s.qempty);
+      base += 2 * n;
+    }
+    if (lane == 0) {
+      tc_commit(&s.done);
+      mbar_wait(&s.done, 0);                               // time bound only
+    }
+    __syncwarp();
+  }
+
+  // -------------------------------------------------------------- softmax
+  static __device__ void softmax(const KvAttnParams& P, S& s, uint32_t tmem) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slot = warp >> 2, r = (warp & 3) * 32 + lane;
+    uint32_t* status = P.b.status;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + TM_S + slot * NK, t_o = tmem + lanes + TM_O + slot * D;
+    const float sl2 = P.scale * kLog2e;
+    const float grow = kGrow / sl2;
+    const int rt = r / P.g, rh = r - rt * P.g;               // token and head of this row
+    int ns = 0, base = 0, no1 = 0;
+    float m = -INFINITY, l = 0.f;
+    bool has_o = false;
+    for (int pieces = 0;; ++pieces) {
+      const int pi = pieces & 1;
+      if (!mbar_wait_warp(&s.pfull[pi], (pieces >> 1) & 1, status, 7)) return;
+      const Piece pc = s.piece[pi];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.pempty[pi]);
+      if (pc.end) return;
+      const int tok = rt + (pc.dual ? slot * P.tt : 0);      // of the item
+      const bool valid = rt < P.tt && tok < pc.ntok;
+      const bool active = __any_sync(0xffffffffu, valid);
+      // keys that the row sees: lo .. hi; rows of no token take all, unstored
+      const int p = pc.pos0 + tok;
+      const int hi = valid ? min(p, pc.len - 1) : 0x7FFFFFFF;
+      const int lo = valid && P.n_win ? p - P.n_win + 1 : (int)0x80000000;
+      // rows of V that no query of the item sees: before its first window, past its end
+      const int vlo = P.n_win ? pc.pos0 - P.n_win + 1 : 0, vhi = pc.len;
+      if (pc.first) {
+        m = -INFINITY;
+        l = 0.f;
+        has_o = false;
+      }
+      const int mine = pc.dual ? pc.n : (pc.n + 1 - slot) / 2;
+      for (int j = 0; j < mine; ++j) {
+        const int vt = base + 2 * (pc.dual ? j : 2 * j + slot) + 1, st = vt % NST;
+        if (!mbar_wait_warp(&s.sready[slot], ns & 1, status, 8)) return;
+        ++ns;
+        if (!mbar_wait_warp(&s.full[st], (vt / NST) & 1, status, 9)) return;
+        const int blk = s.blk[st], kb = blk * NK;
+        if (active) {
+          tc_fence_after();
+          float v[NK];
+          {
+            uint32_t raw[NK];
+#pragma unroll
+            for (int c = 0; c < NK; c += 32) tmem_ld32_nowait(t_s + c, raw + c);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < NK; ++c) v[c] = __uint_as_float(raw[c]);
+          }
+          int hc = hi - kb, lc = lo - kb;                    // columns lc .. hc
+          if (lo == (int)0x80000000) lc = 0;
+          if (SPARSE && valid && !((s.mask[st] >> tok) & 1)) hc = -1;
+          if (blk < 0) hc = -1;
+          if (!__all_sync(0xffffffffu, hc >= NK - 1 && lc <= 0)) {
+#pragma unroll
+            for (int c = 0; c < NK; ++c) v[c] = c <= hc && c >= lc ? v[c] : -INFINITY;
+          }
+          float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
+#pragma unroll
+          for (int c = 4; c < NK; c += 4) {
+            x0 = fmaxf(x0, v[c]);
+            x1 = fmaxf(x1, v[c + 1]);
+            x2 = fmaxf(x2, v[c + 2]);
+            x3 = fmaxf(x3, v[c + 3]);
+          }
+          const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+          const bool up = mx > m + grow;
+          if (__any_sync(0xffffffffu, up)) {
+            const float mn = up ? mx : m;
+            const float a = up ? ex2((m - mn) * sl2) : 1.0f;
+            m = mn;
+            l *= a;
+            if (has_o) {
+              // P V of the block before is complete: its commit came with these scores
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_ld16_nowait(t_o + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                tmem_st16(t_o + c, o);
+              }
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : m * sl2;
+          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+          for (int c = 0; c < NK; c += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float a0 = ex2(fmaf(v[c + e], sl2, -off)), a1 = ex2(fmaf(v[c + e + 1], sl2, -off));
+              const float a2 = ex2(fmaf(v[c + e + 2], sl2, -off)),
+                          a3 = ex2(fmaf(v[c + e + 3], sl2, -off));
+              s0 += a0;
+              s1 += a1;
+              s2 += a2;
+              s3 += a3;
+              pk[e / 2] = pack16<F16>(a0, a1);
+              pk[e / 2 + 1] = pack16<F16>(a2, a3);
+            }
+            tmem_st16(t_s + c / 2, pk);
+          }
+          l += (s0 + s1) + (s2 + s3);
+        }
+        if (blk >= 0 && (kb + NK > vhi || kb < vlo)) {
+          // V rows that nobody sees may hold anything, and 0 x NaN is NaN: zero them
+          const int key = kb + r;
+          if (key >= vhi || key < vlo) {
+            const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(s.kv[st] + c * (MROWS * 128) + r * 128 + e * 16) = z;
+          }
+          fence_proxy_async_smem();
+        }
+        if (active) tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.pready[slot]);
+        has_o = true;
+      }
+      if (mine > 0) {                                        // the last P V
+        if (!mbar_wait_warp(&s.sready[slot], ns & 1, status, 8)) return;
+        ++ns;
+        tc_fence_after();
+      }
+      base += 2 * pc.n;
+      if (!pc.last) continue;
+      // ---------------------------------------------------------- epilogue
+      if (!pc.dual && slot == 1) {
+        s.m1[r] = m;
+        s.l1[r] = has_o ? l : -1.0f;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.o1ready);
+        if (!mbar_wait_warp(&s.o1free, no1 & 1, status, 10)) return;
+        ++no1;
+        continue;
+      }
+      float a0 = 1.0f, a1 = 0.f;
+      bool has1 = false;
+      if (!pc.dual) {
+        if (!mbar_wait_warp(&s.o1ready, no1 & 1, status, 11)) return;
+        ++no1;
+        tc_fence_after();
+        has1 = s.l1[r] >= 0.f || s.l1[r] != s.l1[r];
+        if (has1) {
+          const float m1 = s.m1[r], mm = fmaxf(m, m1), ms = mm == -INFINITY ? 0.f : mm;
+          a0 = ex2((m - ms) * sl2);
+          a1 = ex2((m1 - ms) * sl2);
+          l = l * a0 + s.l1[r] * a1;
+          m = mm;
+        }
+        has1 = __any_sync(0xffffffffu, has1);                // the same in every lane
+      }
+      float top = m * sl2, f = 1.0f;                         // log2 of the largest weight
+      if (pc.part < 0) {
+        const int hq = pc.h * P.g + rh;
+        if (P.sink && valid) {
+          const float sk = P.sink[hq] * kLog2e, mm = fmaxf(top, sk), ms = mm == -INFINITY ? 0.f : mm;
+          f = ex2(top - ms);
+          l = l * f + ex2(sk - ms);
+          top = ms;
+        }
+        if (valid && P.lse)
+          P.lse[(int64_t)(pc.tok0 + tok) * P.Hq + hq] = log_sum(top, l, m == -INFINITY, P.sink, hq);
+        f = l == 0.f ? 0.f : f / l;
+      } else if (valid) {
+        float2* ml = P.part_ml + (int64_t)pc.part * (2 * MROWS) + (pc.dual ? slot * MROWS : 0) + r;
+        *ml = make_float2(top, l);
+      }
+      __syncwarp();
+      if (active) {
+        uint16_t* out = reinterpret_cast<uint16_t*>(const_cast<void*>(P.out.p)) +
+                        (int64_t)(pc.tok0 + tok) * P.out.tok +
+                        (int64_t)(pc.h * P.g + rh) * P.out.head;
+        float* part = P.part_o +
+                      ((int64_t)pc.part * (2 * MROWS) + (pc.dual ? slot * MROWS : 0) + r) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32], o1[32];
+          if (has_o) tmem_ld32_nowait(t_o + c, o);
+          if (has1) tmem_ld32_nowait(t_o + D + c, o1);
+          tmem_ld_wait();
+          float x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            x[e] = has_o ? __uint_as_float(o[e]) * a0 : 0.f;
+            if (has1) x[e] = fmaf(__uint_as_float(o1[e]), a1, x[e]);
+          }
+          if (valid && pc.part < 0) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint4 w;
+              w.x = pack16<F16>(x[e] * f, x[e + 1] * f);
+              w.y = pack16<F16>(x[e + 2] * f, x[e + 3] * f);
+              w.z = pack16<F16>(x[e + 4] * f, x[e + 5] * f);
+              w.w = pack16<F16>(x[e + 6] * f, x[e + 7] * f);
+              *reinterpret_cast<uint4*>(out + c + e) = w;
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(part + c + e) =
+                  make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+      }
+      if (!pc.dual) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.o1free);
+      }
+    }
+  }
+};
+
+}  // namespace
+
+template <int D, bool F16, bool SPARSE>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    kv_attn_kernel(const __grid_constant__ KvAttnParams P, const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v) {
+  using K = Kernel<D, F16, SPARSE>;
+  using S = typename K::S;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < K::NST; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    mbar_init(&s.qfull, 1);
+    mbar_init(&s.qempty, 1);
+    mbar_init(&s.o1ready, 4);
+    mbar_init(&s.o1free, 4);
+    mbar_init(&s.done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.sready[i], 1);
+      mbar_init(&s.pready[i], 4);
+      mbar_init(&s.pfull[i], 1);
+      mbar_init(&s.pempty[i], 9);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 8) tmem_alloc(&s.tmem_base, K::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  if (warp >= 8) {
+    regs_down<kOtherRegs>();
+    if (warp == 9)
+      K::produce(P, s, &tm_q, &tm_k, &tm_v);
+    else if (warp == 8)
+      K::issue(P, s, tmem);
+  } else {
+    regs_up<kSoftmaxRegs>();
+    K::softmax(P, s, tmem);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, K::kCols);
+  }
+}
+
+// Joins the parts of the items that were cut: block (c, y) the item whose first
+// part is CTA c's last piece, 16 of its rows at a time.  Its further parts are
+// the first pieces of the CTAs behind c, in order, so the sums are the same on
+// every run.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) kv_merge_kernel(const __grid_constant__ KvAttnParams P, int n_cta) {
+  const int c = blockIdx.x;
+  const KvPart r = P.parts[2 * c + 1];
+  if (r.rows == 0) return;
+  // the CTA whose first piece ends the item (kKvMaxCtas <= 256 threads look at once)
+  __shared__ int last_s;
+  if (threadIdx.x == 0) last_s = n_cta - 1;
+  __syncthreads();
+  const int cand = c + 1 + threadIdx.x;
+  if (cand < n_cta && P.parts[2 * cand].ends) atomicMin(&last_s, cand);
+  __syncthreads();
+  const int last = last_s;
+  constexpr int kPer = D / 8;            // threads a row, 8 dims each
+  constexpr int kRows = 256 / kPer;
+  const int d0 = (threadIdx.x % kPer) * 8;
+  for (int i = blockIdx.y * kRows + threadIdx.x / kPer; i < r.rows; i += gridDim.y * kRows) {
+    const int tok = i / P.g, hd = i - tok * P.g;
+    const int row = tok / P.tt * MROWS + (tok % P.tt) * P.g + hd;
+    auto place = [&](int q) { return (int64_t)(q == c ? 2 * c + 1 : 2 * q) * (2 * MROWS) + row; };
+    float top = -INFINITY;
+    for (int q = c; q <= last; ++q) top = fmaxf(top, P.part_ml[place(q)].x);
+    const bool none = top == -INFINITY;
+    const int hq = r.h * P.g + hd;
+    const float sk = P.sink ? P.sink[hq] * kLog2e : -INFINITY;
+    top = fmaxf(top, sk);
+    if (top == -INFINITY) top = 0.f;
+    float l = P.sink ? ex2(sk - top) : 0.f, x[8] = {};
+#pragma unroll 4
+    for (int q = c; q <= last; ++q) {
+      const int64_t at = place(q);
+      const float2 ml = P.part_ml[at];
+      const float f = ex2(ml.x - top);
+      const float4 u = *reinterpret_cast<const float4*>(P.part_o + at * D + d0);
+      const float4 v = *reinterpret_cast<const float4*>(P.part_o + at * D + d0 + 4);
+      l += ml.y * f;
+      x[0] += u.x * f;
+      x[1] += u.y * f;
+      x[2] += u.z * f;
+      x[3] += u.w * f;
+      x[4] += v.x * f;
+      x[5] += v.y * f;
+      x[6] += v.z * f;
+      x[7] += v.w * f;
+    }
+    const float f = l == 0.f ? 0.f : 1.0f / l;
+    uint4 w;
+    w.x = pack16<F16>(x[0] * f, x[1] * f);
+    w.y = pack16<F16>(x[2] * f, x[3] * f);
+    w.z = pack16<F16>(x[4] * f, x[5] * f);
+    w.w = pack16<F16>(x[6] * f, x[7] * f);
+    uint16_t* out = reinterpret_cast<uint16_t*>(const_cast<void*>(P.out.p)) +
+                    (int64_t)(r.tok0 + tok) * P.out.tok + (int64_t)hq * P.out.head + d0;
+    *reinterpret_cast<uint4*>(out) = w;
+    if (P.lse && d0 == 0)
+      P.lse[(int64_t)(r.tok0 + tok) * P.Hq + hq] = log_sum(top, l, none, P.sink, hq);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+namespace {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+template <int D, bool F16, bool SPARSE>
+cudaError_t launch(const KvAttnParams& P, const CUtensorMap& q, const CUtensorMap& k,
+                   const CUtensorMap& v, int grid, int dev, cudaStream_t st) {
+  const size_t smem = sizeof(Smem<D, SPARSE>) + 1024;
+  static_assert(sizeof(Smem<D, SPARSE>) + 1024 <= 232448, "shared memory of a CTA");
+  static unsigned long long configured = 0;
+  if (dev >= 64 || !(configured & (1ull << dev))) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kv_attn_kernel<D, F16, SPARSE>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured |= 1ull << dev;
+  }
+  kv_attn_kernel<D, F16, SPARSE><<<grid, NTHREADS, smem, st>>>(P, q, k, v);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  kv_merge_kernel<D, F16><<<dim3(grid, 4), 256, 0, st>>>(P, grid);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attn(const KvAttnParams& params, cudaStream_t st) {
+  KvAttnParams P = params;
+  auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+  if (!enc) return cudaErrorNotSupported;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // tokens a tile: as many as fill its 128 rows; sparse tiles name their tokens
+  // by the bits of a word, 32 for the two tiles
+  P.tt = MROWS / P.g;
+  if (P.sparse && P.tt > 16) P.tt = 16;
+  const CUtensorMapDataType ty =
+      P.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint32_t ones[3] = {1, 1, 1};
+  CUtensorMap mq, mk, mv;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)P.d, (cuuint64_t)P.Hq, (cuuint64_t)P.b.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)P.q.head * 2, (cuuint64_t)P.q.tok * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)P.g, (cuuint32_t)P.tt};
+    if (enc(&mq, ty, 3, const_cast<void*>(P.q.p), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  for (int i = 0; i < 2; ++i) {
+    const cuuint64_t dims[2] = {(cuuint64_t)P.d, (cuuint64_t)(P.b.n_blocks * P.Hkv * NK)};
+    const cuuint64_t strides[1] = {(cuuint64_t)P.d * 2};
+    const cuuint32_t box[2] = {64, NK};
+    if (enc(i ? &mv : &mk, ty, 2, const_cast<void*>(i ? P.v_cache : P.k_cache), dims, strides, box,
+            ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  const int grid = sms < kKvMaxCtas ? sms : kKvMaxCtas;
+#define KV_LAUNCH(D, F) \
+  (P.sparse ? launch<D, F, true>(P, mq, mk, mv, grid, dev, st) \
+            : launch<D, F, false>(P, mq, mk, mv, grid, dev, st))
+  if (P.d == 128) return P.f16 ? KV_LAUNCH(128, true) : KV_LAUNCH(128, false);
+  return P.f16 ? KV_LAUNCH(64, true) : KV_LAUNCH(64, false);
+#undef KV_LAUNCH
 }
 
 }  // namespace v4a

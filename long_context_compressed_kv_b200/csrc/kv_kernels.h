@@ -7,6 +7,10 @@
 namespace v4a {
 
 constexpr int kKvBlock = 128;       // positions a pool block holds
+constexpr int kKvMaxRows = 0x7FFFFF00;   // rows of a pool (TMA coordinates are 32-bit)
+constexpr int kKvMaxSel = 2048;     // entries of a query's block list
+constexpr int kKvMaxCtas = 160;     // CTAs of the attention kernel (one an SM)
+constexpr int kKvPartRows = 256;    // rows of an item: two tiles
 
 // A ragged batch of new tokens over paged caches (see "16-bit K/V layers" in
 // v4attn.h).
@@ -34,6 +38,13 @@ struct KvAppendParams {
   double freq[64];                    // theta^(-2k/d_rope) / (2 pi): turns per position
 };
 
+// A part of an item (rows of one K/V head's queries) whose key blocks were cut.
+struct KvPart {
+  int rows;           // 0: none
+  int ends;           // holds the item's last blocks
+  int h, tok0;        // K/V head, first token row
+};
+
 struct KvAttnParams {
   KvBatch b;
   int Hq, Hkv, g, d, f16;             // g = Hq / Hkv
@@ -46,6 +57,12 @@ struct KvAttnParams {
   int n_lists, n_sel, n_local;
   const float* sink;
   float* lse;
+  int tt = 0;                         // tokens a tile (set at launch)
+  // workspace: two parts a CTA (its first and last pieces), their rows'
+  // (log2 of the largest weight, sum of weights) and unnormalised outputs
+  KvPart* parts;                      // [kKvMaxCtas][2]
+  float2* part_ml;                    // [kKvMaxCtas][2][kKvPartRows]
+  float* part_o;                      // [kKvMaxCtas][2][kKvPartRows][d]
 };
 
 cudaError_t launch_kv_append(const KvAppendParams& P, cudaStream_t st);

@@ -89,7 +89,7 @@ def test_attention_rows_that_are_refused(bad):
 
 
 @pytest.mark.parametrize("bad,want", [
-    (dict(n_sel=-1), INVALID), (dict(n_sel=4097, idx=FAKE), UNSUPPORTED), (dict(n_sel=4), INVALID),
+    (dict(n_sel=-1), INVALID), (dict(n_sel=2049, idx=FAKE), UNSUPPORTED), (dict(n_sel=4), INVALID),
     (dict(n_sel=4, idx=FAKE, n_lists=3), INVALID), (dict(n_sel=4, idx=FAKE, n_local=-1), INVALID),
     (dict(n_sel=4, idx=FAKE + 2), INVALID), (dict(d=desc(n_win=64)), INVALID)])
 def test_lists_that_are_refused(bad, want):
