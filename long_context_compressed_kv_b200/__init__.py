@@ -16,7 +16,7 @@ import torch
 
 from . import _abi
 from ._abi import (BF16, CSA, E4M3_BF16ROPE, F16, F32, HCA, MXFP4, CompressArgs, DecodeArgs,
-                   IndexArgs, KvAppendArgs, KvAttnArgs, KvDesc, LayerDesc, MqaArgs, ProjectArgs)
+                   IndexArgs, KvDesc, LayerDesc, MqaArgs, ProjectArgs)
 
 _lib = _abi.load()
 
@@ -244,6 +244,7 @@ def project(X, W, Y, stream=None):
 
 # ---------------------------------------------------------------- 16-bit K/V layers
 _KV_DTYPES = {torch.bfloat16: BF16, torch.float16: F16}
+_KV_TORCH = {BF16: torch.bfloat16, F16: torch.float16}
 
 
 def kv_desc(Hq: int, Hkv: int, d: int, *, dtype=torch.bfloat16, d_rope: Optional[int] = None,
@@ -269,52 +270,61 @@ def kv_workspace(desc: KvDesc, device="cuda") -> torch.Tensor:
     return ws
 
 
-def _kv_rows(name, t, T, H, desc):
+def _kv_rows(name, t, T, H, d, dtype):
     """(pointer, token stride, head stride) of [T][H][d] rows; their last dim contiguous."""
-    if t.dim() != 3 or tuple(t.shape) != (T, H, desc.d):
-        raise ValueError(f"{name} must be [{T}][{H}][{desc.d}], got {tuple(t.shape)}")
-    if _KV_DTYPES.get(t.dtype) != desc.dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, not the layer's")
-    if t.stride(2) != 1 and t.numel():
+    if t.shape != (T, H, d) or t.dtype is not dtype:
+        raise ValueError(f"{name} must be [{T}][{H}][{d}] in {dtype}, got {tuple(t.shape)} in "
+                         f"{t.dtype}")
+    tok, head, one = t.stride()
+    if one != 1 and T:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     # a dimension of one element may have any stride: it is never taken
-    return (_p(t) if t.numel() else None, t.stride(0) if T > 1 else H * desc.d,
-            t.stride(1) if H > 1 else desc.d)
+    return t.data_ptr(), tok if T > 1 else H * d, head if H > 1 else d
 
 
 def _kv_small(name, t, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got "
                          f"{t.dtype} {tuple(t.shape)}")
-    return _p(t)
+    return t.data_ptr()
 
 
-def _kv_common(desc, T, k_cache, v_cache, q_start, kv_len, block_table, ws, others):
-    """Checked (B, pool and table fields) of a call on a 16-bit K/V layer."""
-    for t in (k_cache, v_cache, q_start, kv_len, block_table, ws, *others):
-        if t is not None and t.device != k_cache.device:
+def _kv_common(d, Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table, ws, others):
+    """Checked (device, B, pool and table fields) of a call on a 16-bit K/V layer."""
+    dev = k_cache.get_device()
+    if dev < 0:
+        raise ValueError("tensor must live on the GPU")
+    for t in (v_cache, q_start, kv_len, block_table, ws, *others):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors on {t.device} and {k_cache.device} in one call")
-    B = int(kv_len.numel())
-    pool = (int(k_cache.shape[0]), desc.Hkv, 128, desc.d)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if _KV_DTYPES.get(t.dtype) != desc.dtype or tuple(t.shape) != pool or \
-                not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {pool} tensor of the layer's dtype, got "
-                             f"{t.dtype} {tuple(t.shape)}")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B][blocks_per_seq]")
-    bps = int(block_table.shape[1])
-    return B, (_p(k_cache), _p(v_cache), pool[0],
-               _kv_small("q_start", q_start, torch.int32, (B + 1,)),
-               _kv_small("kv_len", kv_len, torch.int64, (B,)),
-               _kv_small("block_table", block_table, torch.int32, (B, bps)), bps)
+    B = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    pool = (k_cache.shape[0], Hkv, 128, d)
+    bps = block_table.shape[1] if block_table.dim() == 2 else -1
+    return dev, B, (_kv_small("k_cache", k_cache, dtype, pool),
+                    _kv_small("v_cache", v_cache, dtype, pool), pool[0],
+                    _kv_small("q_start", q_start, torch.int32, (B + 1,)),
+                    _kv_small("kv_len", kv_len, torch.int64, (B,)),
+                    _kv_small("block_table", block_table, torch.int32, (B, bps)), bps)
 
 
-def _kv_call(fn, desc, a, ws, device, stream):
-    # on the tensors' device, whichever is current
-    with torch.cuda.device(device):
-        _check(fn, getattr(_lib, fn)(ctypes.byref(desc), ctypes.byref(a), _p(ws), ws.numel(),
-                                     _stream(stream)))
+_KV_CALLS = {fn: (_abi.packed_call(fn), fmt.pack) for fn, fmt in _abi.PACKED.items()}
+
+
+def _kv_call(fn, desc, dev, ws, stream, *values):
+    call, pack = _KV_CALLS[fn]
+    args, ws_p, ws_n = pack(*values), ws.data_ptr(), ws.numel() * ws.element_size()
+    at = ctypes.addressof(desc)
+    if torch.cuda.current_device() == dev:
+        status = call(at, args, ws_p, ws_n, _raw_stream(dev, stream))
+    else:       # on the tensors' device, whichever is current
+        with torch.cuda.device(dev):
+            status = call(at, args, ws_p, ws_n, _raw_stream(dev, stream))
+    if status != _abi.OK:
+        raise V4AttnError(fn, status)
+
+
+def _raw_stream(dev: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def kv_append(desc: KvDesc, *, k, v, k_cache, v_cache, q_start, kv_len, block_table, ws, q=None,
@@ -325,36 +335,36 @@ def kv_append(desc: KvDesc, *, k, v, k_cache, v_cache, q_start, kv_len, block_ta
     k, v [T][Hkv][d], q [T][Hq][d] (strided views allowed); k_cache, v_cache
     [n_blocks][Hkv][128][d]; q_start int32 [B + 1], kv_len int64 [B] (new tokens
     included), block_table int32 [B][blocks_per_seq]."""
-    T = int(k.shape[0])
-    B, cache = _kv_common(desc, T, k_cache, v_cache, q_start, kv_len, block_table, ws,
-                          (k, v, q, q_out))
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    none = (None, 0, 0)
-    a = KvAppendArgs(T, B, *_kv_rows("k", k, T, desc.Hkv, desc),
-                     *_kv_rows("v", v, T, desc.Hkv, desc),
-                     *(none if q is None else _kv_rows("q", q, T, desc.Hq, desc)),
-                     *(none if q is None else _kv_rows("q_out", q_out, T, desc.Hq, desc)), *cache)
-    _kv_call("v4attn_kv_append", desc, a, ws, k_cache.device, stream)
+    d, Hkv, dtype, T = desc.d, desc.Hkv, _KV_TORCH.get(desc.dtype), k.shape[0]
+    dev, B, cache = _kv_common(d, Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table, ws,
+                               (k, v, q, q_out))
+    if q is None:
+        rows = (0, 0, 0, 0, 0, 0)
+    else:
+        rows = (*_kv_rows("q", q, T, desc.Hq, d, dtype),
+                *_kv_rows("q_out", q_out, T, desc.Hq, d, dtype))
+    _kv_call("v4attn_kv_append", desc, dev, ws, stream, T, B, *_kv_rows("k", k, T, Hkv, d, dtype),
+             *_kv_rows("v", v, T, Hkv, d, dtype), *rows, *cache)
 
 
 def _kv_attention(fn, desc, q, k_cache, v_cache, q_start, kv_len, block_table, out, ws, lse, sink,
                   idx, n_local, stream):
-    T = int(q.shape[0])
-    B, cache = _kv_common(desc, T, k_cache, v_cache, q_start, kv_len, block_table, ws,
-                          (q, out, lse, sink, idx))
-    lists = (None, 1, 0)
+    d, Hq, dtype, T = desc.d, desc.Hq, _KV_TORCH.get(desc.dtype), q.shape[0]
+    dev, B, cache = _kv_common(d, desc.Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table,
+                               ws, (q, out, lse, sink, idx))
+    n_lists, n_sel = 1, 0
     if idx is not None:
-        if idx.dim() == 2:
-            idx = idx[:, None]
-        if idx.dim() != 3:
-            raise ValueError("idx must be [T][n_lists][n_sel] or [T][n_sel]")
-        lists = (_kv_small("idx", idx, torch.int32, (T, *idx.shape[1:])), *idx.shape[1:])
-    a = KvAttnArgs(T, B, *_kv_rows("q", q, T, desc.Hq, desc), *cache, *lists, n_local,
-                   None if sink is None else _kv_small("sink", sink, torch.float32, (desc.Hq,)),
-                   *_kv_rows("out", out, T, desc.Hq, desc),
-                   None if lse is None else _kv_small("lse", lse, torch.float32, (T, desc.Hq)))
-    _kv_call(fn, desc, a, ws, k_cache.device, stream)
+        n_lists = idx.shape[1] if idx.dim() == 3 else 1
+        n_sel = idx.shape[-1] if idx.dim() else 0
+        idx = _kv_small("idx", idx, torch.int32,
+                        (T, n_lists, n_sel) if idx.dim() == 3 else (T, n_sel))
+    _kv_call(fn, desc, dev, ws, stream, T, B, *_kv_rows("q", q, T, Hq, d, dtype), *cache,
+             idx or 0, n_lists, n_sel, n_local,
+             0 if sink is None else _kv_small("sink", sink, torch.float32, (Hq,)),
+             *_kv_rows("out", out, T, Hq, d, dtype),
+             0 if lse is None else _kv_small("lse", lse, torch.float32, (T, Hq)))
 
 
 def paged_attention(desc: KvDesc, *, q, k_cache, v_cache, q_start, kv_len, block_table, out, ws,

@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libv4attn.so")
@@ -104,6 +105,19 @@ STRUCTS = {"v4attn_layer_desc": LayerDesc, "v4attn_compress_args": CompressArgs,
            "v4attn_kv_desc": KvDesc, "v4attn_kv_append_args": KvAppendArgs,
            "v4attn_kv_attn_args": KvAttnArgs}
 
+# argument blocks of the short calls, packed from plain values in one go (a
+# ctypes structure of 25 fields takes 2 us to fill, its packed bytes 0.5 us)
+_CODES = {c_i32: "i", c_i64: "q", c_f32: "f", c_ptr: "P"}
+
+
+def packer(cls) -> struct.Struct:
+    """The struct.Struct that lays values out as ``cls`` does."""
+    return struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_) + "0q")
+
+
+PACKED = {"v4attn_kv_append": packer(KvAppendArgs), "v4attn_paged_attention": packer(KvAttnArgs),
+          "v4attn_block_sparse_attention": packer(KvAttnArgs)}
+
 # entry point -> (restype, argtypes)
 SIGNATURES = {
     "v4attn_workspace_size": (c_sz, [ctypes.POINTER(LayerDesc), c_i32, c_i64]),
@@ -160,3 +174,11 @@ def load() -> ctypes.CDLL:
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+def packed_call(name: str):
+    """The entry point ``name`` taking (desc address, packed arguments, ws, ws bytes, stream)."""
+    fn = load()[name]           # a function object of its own, unlike the attribute
+    fn.restype = ctypes.c_int
+    fn.argtypes = [c_ptr, ctypes.c_char_p, c_ptr, c_sz, c_ptr]
+    return fn

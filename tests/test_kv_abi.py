@@ -96,6 +96,16 @@ def test_lists_that_are_refused(bad, want):
     assert attention("v4attn_block_sparse_attention", **bad) == want
 
 
+def test_packed_arguments_lie_as_the_structures_do():
+    for name, cls in (("v4attn_kv_append", _abi.KvAppendArgs),
+                      ("v4attn_paged_attention", _abi.KvAttnArgs)):
+        values = list(range(1, len(cls._fields_) + 1))
+        raw = _abi.PACKED[name].pack(*values)
+        assert len(raw) == ctypes.sizeof(cls)
+        got = cls.from_buffer_copy(raw)
+        assert [getattr(got, f) for f, _ in cls._fields_] == values
+
+
 def test_nothing_to_do_is_no_error():
     assert append(T=0, k=None, v=None) == _abi.OK
     assert attention(T=0, q=None, out=None) == _abi.OK
