@@ -48,6 +48,11 @@ constexpr int kWindow = 2048;                  // blocks whose selection is join
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.0f;                  // log2 of the growth that rescales O
+// 2^f on [-1/2, 1/2] (see exp2_pair)
+constexpr float kExp0 = 0.999999285f, kExp1 = 0.693121791f, kExp2 = 0.240247443f,
+                kExp3 = 0.0559178591f, kExp4 = 0.00957010221f;
+// of 8 pairs of columns, those whose exponentials the FMA units form
+constexpr uint32_t kEmulated = 0x88;
 // cost of an item besides its blocks, in blocks (Q load, epilogue)
 constexpr int kItemCost = 1;
 // least cost of a CTA's range
@@ -65,6 +70,14 @@ struct Piece {
   int end;           // no piece: the CTA is done
 };
 
+// The scores that a slot's warps find ready.
+struct Step {
+  int tile;          // ring count of the block's V tile, -1: no scores, the piece's O is complete
+  int blk;           // logical block, -1: not to be seen
+  uint32_t mask;     // the item's tokens that take it (sparse)
+};
+constexpr int kMeta = 16;
+
 template <int D, bool SPARSE>
 struct Cfg {
   static constexpr int kTile = MROWS * D * 2;           // bytes of a Q, K or V tile
@@ -79,8 +92,10 @@ struct Smem {
   alignas(1024) uint8_t kv[C::kStages][C::kTile];
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t qfull, qempty, sready[2], pready[2], pfull[2], pempty[2], o1ready, o1free, done;
-  int blk[C::kStages];             // logical block of a V stage, -1: not to be seen
-  uint32_t mask[C::kStages];       // its tokens (sparse)
+  // of the blocks on their way, by their count (a ring longer than they can be ahead):
+  int blk[kMeta];                  // logical block, -1: not to be seen
+  uint32_t mask[kMeta];            // its tokens (sparse)
+  Step step[2];                    // what the MMA thread says with each slot's scores
   Piece piece[2];
   float m1[MROWS], l1[MROWS];      // slot 1's statistics for the merge in the CTA
   uint32_t tmem_base;
@@ -114,6 +129,54 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// two fp32 lanes an instruction
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// largest of three, NaN if one is
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 2^x of two finite x <= 127 without the SFU: x = n + f, n the nearest integer
+// (adding 1.5 2^23 leaves n in the low mantissa bits), 2^f on [-1/2, 1/2] by a
+// degree-4 polynomial fitted to the least largest relative error (2.4e-6, no
+// bias to speak of), n added to the exponent.  Below 2^-125 the result stays
+// there (a weight that no sum of a row's weights, at least 2^-8, can feel).
+__device__ __forceinline__ void exp2_pair(uint64_t x2, float& y0, float& y1) {
+  const float kMagic = 12582912.0f;
+  float a, b;
+  unpair(x2, a, b);
+  const uint64_t x = pair(fmaxf(a, -125.0f), fmaxf(b, -125.0f));
+  const uint64_t t = add2(x, pair(kMagic, kMagic));
+  const uint64_t n = add2(t, pair(-kMagic, -kMagic));
+  const uint64_t f = fma2(n, pair(-1.0f, -1.0f), x);
+  uint64_t p = fma2(f, pair(kExp4, kExp4), pair(kExp3, kExp3));
+  p = fma2(p, f, pair(kExp2, kExp2));
+  p = fma2(p, f, pair(kExp1, kExp1));
+  p = fma2(p, f, pair(kExp0, kExp0));
+  float p0, p1, t0, t1;
+  unpair(p, p0, p1);
+  unpair(t, t0, t1);
+  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
 template <bool F16>
 __device__ __forceinline__ uint32_t pack16(float x, float y) {
@@ -307,9 +370,9 @@ struct Kernel {
         const int st = it % NST, u = it / NST;
         if (u >= 1 && !mbar_wait_warp(&s.empty[st], (u - 1) & 1, status, 1)) return false;
         if (lane == 0) {
-          if (j == 1) {
-            s.blk[st] = pb < 0 ? -1 : lb;
-            s.mask[st] = mask;
+          if (j == 0) {
+            s.blk[(it >> 1) % kMeta] = pb < 0 ? -1 : lb;
+            s.mask[(it >> 1) % kMeta] = mask;
           }
           mbar_arrive_expect_tx(&s.full[st], C::kTile);
 #pragma unroll
@@ -509,17 +572,24 @@ struct Kernel {
       const int w1 = min(e1, w0 + kWindow);
       for (int i = lane; i < w1 - w0; i += 32) s.list_mask[i] = 0;
       __syncwarp();
-      for (int t = 0; t < pc.ntok; ++t) {
-        const int p = min(pc.pos0 + t, pc.len - 1), last = p < 0 ? -1 : p / NK;
+      if (lane < pc.ntok) {                                    // a lane a token
+        const int p = min(pc.pos0 + lane, pc.len - 1), last = p < 0 ? -1 : p / NK;
         const int local = max(0, last - P.n_local + 1);
+        const int32_t* list = list_of(lane);
         int before = -1;
-        for (int i = 0; i < P.n_sel; i += 32) {
-          bool good;
-          const int e = entries(list_of(t), i, last, before, good);
-          if (good && e >= w0 && e < w1) atomicOr(&s.list_mask[e - w0], 1u << t);
+        for (int i = 0; i < P.n_sel; i += 8) {
+          int e[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = i + j < P.n_sel ? __ldg(list + i + j) : -1;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (e[j] > before && e[j] <= last && e[j] >= w0 && e[j] < w1)
+              atomicOr(&s.list_mask[e[j] - w0], 1u << lane);
+            before = max(before, e[j]);
+          }
         }
-        for (int e = max(local, w0) + lane; e <= last && e < w1; e += 32)
-          atomicOr(&s.list_mask[e - w0], 1u << t);
+        for (int e = max(local, w0); e <= last && e < w1; ++e)
+          atomicOr(&s.list_mask[e - w0], 1u << lane);
       }
       __syncwarp();
       int n = 0;
@@ -606,60 +676,67 @@ struct Kernel {
         if (!mbar_wait_warp(&s.qfull, items & 1, status, 5)) break;
         ++items;
       }
-      auto wait_p = [&](int slot) {
-        const bool r = mbar_wait_warp(&s.pready[slot], np[slot] & 1, status, 6);
-        ++np[slot];
-        return r;
+      // The slot's scores (or, tile < 0, its piece's O) will be complete: said by
+      // this thread's arrive, with what they are of, and the tensor core's.
+      auto signal = [&](int slot, int tile, int blk, uint32_t mask) {
+        if (lane == 0) {
+          s.step[slot] = Step{tile, blk, mask};
+          mbar_arrive(&s.sready[slot]);
+          tc_commit(&s.sready[slot]);
+        }
       };
-      // block i's K at tile base + 2 i, its V at base + 2 i + 1
-      if (dual) {
-        if (n > 0) {
-          if (!(ok = wait_tile(base))) break;
-          qk(0, 0, base);
-          commit(&s.sready[0]);
-          qk(1, 1, base);
-          commit(&s.sready[1]);
-          commit(&s.empty[base % NST]);
-        }
-        for (int i = 0; ok && i < n; ++i) {
-          const int vt = base + 2 * i + 1, kt = vt + 1;
+      int pend[2] = {-1, -1};                              // V tile of the P V still to issue
+      auto flush = [&](int slot) -> bool {
+        if (pend[slot] < 0) return true;
+        if (!mbar_wait_warp(&s.pready[slot], np[slot] & 1, status, 6)) return false;
+        ++np[slot];
+        if (!wait_tile(pend[slot])) return false;
+        pv(slot, pend[slot]);
+        pend[slot] = -1;
+        return true;
+      };
+      const uint32_t tile_bits = (1u << min(P.tt, 31)) - 1;
+      for (int i = 0; ok && i < n; ++i) {
+        const int kt = base + 2 * i, vt = kt + 1, mi = (kt >> 1) % kMeta;
+        if (dual) {
+          int blk = 0;
+          uint32_t mask = 0;
+#pragma unroll
           for (int slot = 0; slot < 2; ++slot) {
-            if (!(ok = wait_p(slot))) break;
-            if (slot == 0 && !(ok = wait_tile(vt))) break;
-            pv(slot, vt);
-            if (i + 1 < n) {
-              if (slot == 0 && !(ok = wait_tile(kt))) break;
-              if (slot == 1) commit(&s.empty[vt % NST]);
-              qk(slot, slot, kt);
+            if (!(ok = flush(slot))) break;
+            if (slot == 0) {
+              if (!(ok = wait_tile(kt))) break;
+              blk = s.blk[mi];
+              mask = s.mask[mi];
+            } else if (i > 0) {
+              commit(&s.empty[(vt - 2) % NST]);            // both slots' P V of the block before
             }
-            commit(&s.sready[slot]);
+            if (!SPARSE || ((mask >> (slot * P.tt)) & tile_bits)) {
+              qk(slot, slot, kt);
+              signal(slot, vt, blk, mask);
+              pend[slot] = vt;
+            }
           }
-          if (!ok) break;
-          if (i + 1 < n)
-            commit(&s.empty[kt % NST]);
-          else
-            commit(&s.empty[vt % NST]);
-        }
-      } else {
-        for (int i = 0; ok && i < n && i < 2; ++i) {
-          if (!(ok = wait_tile(base + 2 * i))) break;
-          qk(i, 0, base + 2 * i);
-          commit(&s.sready[i]);
-          commit(&s.empty[(base + 2 * i) % NST]);
-        }
-        for (int i = 0; ok && i < n; ++i) {
-          const int slot = i & 1, vt = base + 2 * i + 1, kt = base + 2 * (i + 2);
-          if (!(ok = wait_p(slot)) || !(ok = wait_tile(vt))) break;
-          pv(slot, vt);
-          commit(&s.empty[vt % NST]);
-          if (i + 2 < n) {
-            if (!(ok = wait_tile(kt))) break;
-            qk(slot, 0, kt);
-            commit(&s.empty[kt % NST]);
-          }
-          commit(&s.sready[slot]);
+          if (ok) commit(&s.empty[kt % NST]);
+        } else {
+          const int slot = i & 1;
+          if (!(ok = flush(slot))) break;
+          if (i > 1) commit(&s.empty[(vt - 4) % NST]);
+          if (!(ok = wait_tile(kt))) break;
+          qk(slot, 0, kt);
+          commit(&s.empty[kt % NST]);
+          signal(slot, vt, s.blk[mi], s.mask[mi]);
+          pend[slot] = vt;
         }
       }
+      for (int j = 0; ok && j < 2; ++j) {                  // the older block first
+        const int slot = dual ? j : (n + j) & 1;
+        ok = flush(slot);
+        if (!ok) break;
+        signal(slot, -1, 0, 0);
+        if (!dual && n + j >= 2) commit(&s.empty[(base + 2 * (n + j - 2) + 1) % NST]);
+      }
+      if (ok && dual && n > 0) commit(&s.empty[(base + 2 * n - 1) % NST]);
       if (!ok) break;
       if (last) commit(&s.qempty);
       base += 2 * n;
@@ -672,6 +749,40 @@ struct Kernel {
   }
 
   // -------------------------------------------------------------- softmax
+  // The row's weights 2^(v sl2 - off) to its P columns; returns their sum.
+  template <bool EMULATE>
+  static __device__ __forceinline__ float weights(const float* v, float sl2, float off,
+                                                  uint32_t t_p, uint32_t kp) {
+    const uint64_t scale = pair(sl2, sl2), shift = pair(-off, -off);
+    uint64_t s0 = 0, s1 = 0;                                 // two pairs of zeros
+#pragma unroll
+    for (int c = 0; c < NK; c += 32) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        const uint64_t x = fma2(pair(v[c + e], v[c + e + 1]), scale, shift);
+        float a, b;
+        if (EMULATE && ((kEmulated >> (e / 2 % 8)) & 1)) {
+          exp2_pair(x, a, b);
+        } else {
+          unpair(x, a, b);
+          a = ex2(a);
+          b = ex2(b);
+        }
+        if (e & 2)
+          s1 = add2(s1, pair(a, b));
+        else
+          s0 = add2(s0, pair(a, b));
+        pk[e / 2] = pack16<F16>(a, b);
+        if (SPARSE) pk[e / 2] &= kp;
+      }
+      tmem_st16(t_p + c / 2, pk);
+    }
+    float a, b;
+    unpair(add2(s0, s1), a, b);
+    return a + b;
+  }
+
   static __device__ void softmax(const KvAttnParams& P, S& s, uint32_t tmem) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slot = warp >> 2, r = (warp & 3) * 32 + lane;
@@ -681,16 +792,19 @@ struct Kernel {
     const float sl2 = P.scale * kLog2e;
     const float grow = kGrow / sl2;
     const int rt = r / P.g, rh = r - rt * P.g;               // token and head of this row
-    int ns = 0, base = 0, no1 = 0;
+    int ns = 0, no1 = 0;
     float m = -INFINITY, l = 0.f;
     bool has_o = false;
     for (int pieces = 0;; ++pieces) {
       const int pi = pieces & 1;
       if (!mbar_wait_warp(&s.pfull[pi], (pieces >> 1) & 1, status, 7)) return;
-      const Piece pc = s.piece[pi];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.pempty[pi]);
+      const Piece& pc = s.piece[pi];
       if (pc.end) return;
+      // the piece's entry is handed back when the warp has finished with it
+      auto release = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.pempty[pi]);
+      };
       const int tok = rt + (pc.dual ? slot * P.tt : 0);      // of the item
       const bool valid = rt < P.tt && tok < pc.ntok;
       const bool active = __any_sync(0xffffffffu, valid);
@@ -705,15 +819,14 @@ struct Kernel {
         l = 0.f;
         has_o = false;
       }
-      const int mine = pc.dual ? pc.n : (pc.n + 1 - slot) / 2;
-      for (int j = 0; j < mine; ++j) {
-        const int vt = base + 2 * (pc.dual ? j : 2 * j + slot) + 1, st = vt % NST;
+      for (;;) {
         if (!mbar_wait_warp(&s.sready[slot], ns & 1, status, 8)) return;
         ++ns;
-        if (!mbar_wait_warp(&s.full[st], (vt / NST) & 1, status, 9)) return;
-        const int blk = s.blk[st], kb = blk * NK;
+        const Step stp = s.step[slot];
+        tc_fence_after();
+        if (stp.tile < 0) break;                             // the last P V is complete
+        const int blk = stp.blk, kb = blk * NK;
         if (active) {
-          tc_fence_after();
           float v[NK];
           {
             uint32_t raw[NK];
@@ -723,23 +836,22 @@ struct Kernel {
 #pragma unroll
             for (int c = 0; c < NK; ++c) v[c] = __uint_as_float(raw[c]);
           }
-          int hc = hi - kb, lc = lo - kb;                    // columns lc .. hc
-          if (lo == (int)0x80000000) lc = 0;
-          if (SPARSE && valid && !((s.mask[st] >> tok) & 1)) hc = -1;
-          if (blk < 0) hc = -1;
-          if (!__all_sync(0xffffffffu, hc >= NK - 1 && lc <= 0)) {
+          // columns lc .. hc are seen; keep: the row's token takes the block
+          const int hc = hi - kb, lc = lo == (int)0x80000000 ? 0 : lo - kb;
+          const bool keep = blk >= 0 && (!SPARSE || !valid || ((stp.mask >> tok) & 1));
+          const bool edge = __any_sync(0xffffffffu, blk < 0 || (keep && (hc < NK - 1 || lc > 0)));
+          if (edge) {
 #pragma unroll
-            for (int c = 0; c < NK; ++c) v[c] = c <= hc && c >= lc ? v[c] : -INFINITY;
+            for (int c = 0; c < NK; ++c) v[c] = keep && c <= hc && c >= lc ? v[c] : -INFINITY;
           }
-          float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
+          float x0 = max3(v[0], v[1], v[2]), x1 = max3(v[3], v[4], v[5]);
 #pragma unroll
-          for (int c = 4; c < NK; c += 4) {
-            x0 = fmaxf(x0, v[c]);
-            x1 = fmaxf(x1, v[c + 1]);
-            x2 = fmaxf(x2, v[c + 2]);
-            x3 = fmaxf(x3, v[c + 3]);
+          for (int c = 6; c < NK - 2; c += 4) {
+            x0 = max3(x0, v[c], v[c + 1]);
+            x1 = max3(x1, v[c + 2], v[c + 3]);
           }
-          const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+          float mx = max3(x0, x1, max3(v[NK - 2], v[NK - 1], x0));
+          if (SPARSE && !keep) mx = -INFINITY;
           const bool up = mx > m + grow;
           if (__any_sync(0xffffffffu, up)) {
             const float mn = up ? mx : m;
@@ -760,29 +872,19 @@ struct Kernel {
             }
           }
           const float off = m == -INFINITY ? 0.f : m * sl2;
-          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-          for (int c = 0; c < NK; c += 32) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float a0 = ex2(fmaf(v[c + e], sl2, -off)), a1 = ex2(fmaf(v[c + e + 1], sl2, -off));
-              const float a2 = ex2(fmaf(v[c + e + 2], sl2, -off)),
-                          a3 = ex2(fmaf(v[c + e + 3], sl2, -off));
-              s0 += a0;
-              s1 += a1;
-              s2 += a2;
-              s3 += a3;
-              pk[e / 2] = pack16<F16>(a0, a1);
-              pk[e / 2 + 1] = pack16<F16>(a2, a3);
-            }
-            tmem_st16(t_s + c / 2, pk);
-          }
-          l += (s0 + s1) + (s2 + s3);
+          // the SFU gives four exponentials a cycle to an SM quarter and bounds
+          // the whole: part of them are formed by the FMA units, unless a score
+          // is masked, infinite or NaN
+          const uint32_t kp = keep ? 0xffffffffu : 0u;
+          const float sum = edge || __any_sync(0xffffffffu, !(mx <= 3.4e38f))
+                                ? weights<false>(v, sl2, off, t_s, kp)
+                                : weights<true>(v, sl2, off, t_s, kp);
+          l += SPARSE && !keep ? 0.f : sum;
         }
         if (blk >= 0 && (kb + NK > vhi || kb < vlo)) {
           // V rows that nobody sees may hold anything, and 0 x NaN is NaN: zero them
-          const int key = kb + r;
+          const int key = kb + r, st = stp.tile % NST;
+          if (!mbar_wait_warp(&s.full[st], (stp.tile / NST) & 1, status, 9)) return;
           if (key >= vhi || key < vlo) {
             const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -799,13 +901,10 @@ struct Kernel {
         if (lane == 0) mbar_arrive(&s.pready[slot]);
         has_o = true;
       }
-      if (mine > 0) {                                        // the last P V
-        if (!mbar_wait_warp(&s.sready[slot], ns & 1, status, 8)) return;
-        ++ns;
-        tc_fence_after();
+      if (!pc.last) {
+        release();
+        continue;
       }
-      base += 2 * pc.n;
-      if (!pc.last) continue;
       // ---------------------------------------------------------- epilogue
       if (!pc.dual && slot == 1) {
         s.m1[r] = m;
@@ -815,6 +914,7 @@ struct Kernel {
         if (lane == 0) mbar_arrive(&s.o1ready);
         if (!mbar_wait_warp(&s.o1free, no1 & 1, status, 10)) return;
         ++no1;
+        release();
         continue;
       }
       float a0 = 1.0f, a1 = 0.f;
@@ -833,8 +933,9 @@ struct Kernel {
         }
         has1 = __any_sync(0xffffffffu, has1);                // the same in every lane
       }
+      const int part = pc.part;
       float top = m * sl2, f = 1.0f;                         // log2 of the largest weight
-      if (pc.part < 0) {
+      if (part < 0) {
         const int hq = pc.h * P.g + rh;
         if (P.sink && valid) {
           const float sk = P.sink[hq] * kLog2e, mm = fmaxf(top, sk), ms = mm == -INFINITY ? 0.f : mm;
@@ -846,7 +947,7 @@ struct Kernel {
           P.lse[(int64_t)(pc.tok0 + tok) * P.Hq + hq] = log_sum(top, l, m == -INFINITY, P.sink, hq);
         f = l == 0.f ? 0.f : f / l;
       } else if (valid) {
-        float2* ml = P.part_ml + (int64_t)pc.part * (2 * MROWS) + (pc.dual ? slot * MROWS : 0) + r;
+        float2* ml = P.part_ml + (int64_t)part * (2 * MROWS) + (pc.dual ? slot * MROWS : 0) + r;
         *ml = make_float2(top, l);
       }
       __syncwarp();
@@ -854,23 +955,25 @@ struct Kernel {
         uint16_t* out = reinterpret_cast<uint16_t*>(const_cast<void*>(P.out.p)) +
                         (int64_t)(pc.tok0 + tok) * P.out.tok +
                         (int64_t)(pc.h * P.g + rh) * P.out.head;
-        float* part = P.part_o +
-                      ((int64_t)pc.part * (2 * MROWS) + (pc.dual ? slot * MROWS : 0) + r) * D;
+        float* part_o = P.part_o +
+                        ((int64_t)part * (2 * MROWS) + (pc.dual ? slot * MROWS : 0) + r) * D;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32], o1[32];
-          if (has_o) tmem_ld32_nowait(t_o + c, o);
-          if (has1) tmem_ld32_nowait(t_o + D + c, o1);
-          tmem_ld_wait();
-          float x[32];
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16], o1[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            x[e] = has_o ? __uint_as_float(o[e]) * a0 : 0.f;
+          for (int e = 0; e < 16; ++e) o[e] = o1[e] = 0;
+          if (has_o) tmem_ld16_nowait(t_o + c, o);
+          if (has1) tmem_ld16_nowait(t_o + D + c, o1);
+          tmem_ld_wait();
+          float x[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            x[e] = __uint_as_float(o[e]) * a0;
             if (has1) x[e] = fmaf(__uint_as_float(o1[e]), a1, x[e]);
           }
-          if (valid && pc.part < 0) {
+          if (valid && part < 0) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
+            for (int e = 0; e < 16; e += 8) {
               uint4 w;
               w.x = pack16<F16>(x[e] * f, x[e + 1] * f);
               w.y = pack16<F16>(x[e + 2] * f, x[e + 3] * f);
@@ -880,8 +983,8 @@ struct Kernel {
             }
           } else if (valid) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(part + c + e) =
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(part_o + c + e) =
                   make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
           }
           __syncwarp();
@@ -892,6 +995,7 @@ struct Kernel {
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.o1free);
       }
+      release();
     }
   }
 };
@@ -919,7 +1023,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(&s.o1free, 4);
     mbar_init(&s.done, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.sready[i], 1);
+      mbar_init(&s.sready[i], 2);
       mbar_init(&s.pready[i], 4);
       mbar_init(&s.pfull[i], 1);
       mbar_init(&s.pempty[i], 9);
@@ -934,6 +1038,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up
   if (warp >= 8) {
     regs_down<kOtherRegs>();
     if (warp == 9)
@@ -953,11 +1058,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 }
 
 // Joins the parts of the items that were cut: block (c, y) the item whose first
-// part is CTA c's last piece, 16 of its rows at a time.  Its further parts are
-// the first pieces of the CTAs behind c, in order, so the sums are the same on
-// every run.
+// part is CTA c's last piece, some of its rows.  Its further parts are the first
+// pieces of the CTAs behind c; the sums are taken in one order on every run.
+// Launched while the kernel before still runs, it waits for its end here: the
+// parts are small and in L2, so its launch would cost as much as its work.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) kv_merge_kernel(const __grid_constant__ KvAttnParams P, int n_cta) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
   const KvPart r = P.parts[2 * c + 1];
   if (r.rows == 0) return;
@@ -969,26 +1076,26 @@ __global__ void __launch_bounds__(256) kv_merge_kernel(const __grid_constant__ K
   if (cand < n_cta && P.parts[2 * cand].ends) atomicMin(&last_s, cand);
   __syncthreads();
   const int last = last_s;
-  constexpr int kPer = D / 8;            // threads a row, 8 dims each
-  constexpr int kRows = 256 / kPer;
-  const int d0 = (threadIdx.x % kPer) * 8;
-  for (int i = blockIdx.y * kRows + threadIdx.x / kPer; i < r.rows; i += gridDim.y * kRows) {
+  // 256 threads: D / 8 to a row's dims, `lanes` to its parts, the rest to rows
+  constexpr int kPer = D / 8;
+  const int n_part = last - c + 1;
+  const int lanes = n_part > 16 ? 16 : n_part > 4 ? 4 : 1, rows = 256 / kPer / lanes;
+  const int d0 = (threadIdx.x % kPer) * 8, pl = threadIdx.x / kPer % lanes,
+            rl = threadIdx.x / kPer / lanes;
+  __shared__ float xs[256][9], ts[256];
+  for (int i0 = blockIdx.y * rows; i0 < r.rows; i0 += gridDim.y * rows) {
+    const int i = min(i0 + rl, r.rows - 1);
     const int tok = i / P.g, hd = i - tok * P.g;
     const int row = tok / P.tt * MROWS + (tok % P.tt) * P.g + hd;
     auto place = [&](int q) { return (int64_t)(q == c ? 2 * c + 1 : 2 * q) * (2 * MROWS) + row; };
-    float top = -INFINITY;
-    for (int q = c; q <= last; ++q) top = fmaxf(top, P.part_ml[place(q)].x);
-    const bool none = top == -INFINITY;
-    const int hq = r.h * P.g + hd;
-    const float sk = P.sink ? P.sink[hq] * kLog2e : -INFINITY;
-    top = fmaxf(top, sk);
-    if (top == -INFINITY) top = 0.f;
-    float l = P.sink ? ex2(sk - top) : 0.f, x[8] = {};
+    float top = -INFINITY, l = 0.f, x[8] = {};
+    for (int q = c + pl; q <= last; q += lanes) top = fmaxf(top, P.part_ml[place(q)].x);
+    const float off = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
-    for (int q = c; q <= last; ++q) {
+    for (int q = c + pl; q <= last; q += lanes) {
       const int64_t at = place(q);
       const float2 ml = P.part_ml[at];
-      const float f = ex2(ml.x - top);
+      const float f = ex2(ml.x - off);
       const float4 u = *reinterpret_cast<const float4*>(P.part_o + at * D + d0);
       const float4 v = *reinterpret_cast<const float4*>(P.part_o + at * D + d0 + 4);
       l += ml.y * f;
@@ -1001,17 +1108,51 @@ __global__ void __launch_bounds__(256) kv_merge_kernel(const __grid_constant__ K
       x[6] += v.z * f;
       x[7] += v.w * f;
     }
-    const float f = l == 0.f ? 0.f : 1.0f / l;
-    uint4 w;
-    w.x = pack16<F16>(x[0] * f, x[1] * f);
-    w.y = pack16<F16>(x[2] * f, x[3] * f);
-    w.z = pack16<F16>(x[4] * f, x[5] * f);
-    w.w = pack16<F16>(x[6] * f, x[7] * f);
-    uint16_t* out = reinterpret_cast<uint16_t*>(const_cast<void*>(P.out.p)) +
-                    (int64_t)(r.tok0 + tok) * P.out.tok + (int64_t)hq * P.out.head + d0;
-    *reinterpret_cast<uint4*>(out) = w;
-    if (P.lse && d0 == 0)
-      P.lse[(int64_t)(r.tok0 + tok) * P.Hq + hq] = log_sum(top, l, none, P.sink, hq);
+    if (lanes > 1) {                     // the lanes' sums, in the lanes' order
+      __syncthreads();
+      ts[threadIdx.x] = top;
+      xs[threadIdx.x][8] = l;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xs[threadIdx.x][e] = x[e];
+      __syncthreads();
+      if (pl == 0) {
+        for (int k = 1; k < lanes; ++k) top = fmaxf(top, ts[threadIdx.x + k * kPer]);
+        const float o2 = top == -INFINITY ? 0.f : top;
+        const float f0 = ex2(off - o2);
+        l *= f0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= f0;
+        for (int k = 1; k < lanes; ++k) {
+          const int o = threadIdx.x + k * kPer;
+          const float f = ts[o] == -INFINITY ? 0.f : ex2(ts[o] - o2);
+          l += xs[o][8] * f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] += xs[o][e] * f;
+        }
+      }
+    }
+    if (pl == 0 && i0 + rl < r.rows) {
+      const int hq = r.h * P.g + hd;
+      const bool none = top == -INFINITY;
+      float f = 1.0f, log_top = none ? 0.f : top;
+      if (P.sink) {
+        const float sk = P.sink[hq] * kLog2e, t2 = fmaxf(top, sk), z = t2 == -INFINITY ? 0.f : t2;
+        f = ex2(top - z);
+        l = l * f + ex2(sk - z);
+        log_top = z;
+      }
+      f = l == 0.f ? 0.f : f / l;
+      uint4 w;
+      w.x = pack16<F16>(x[0] * f, x[1] * f);
+      w.y = pack16<F16>(x[2] * f, x[3] * f);
+      w.z = pack16<F16>(x[4] * f, x[5] * f);
+      w.w = pack16<F16>(x[6] * f, x[7] * f);
+      uint16_t* out = reinterpret_cast<uint16_t*>(const_cast<void*>(P.out.p)) +
+                      (int64_t)(r.tok0 + tok) * P.out.tok + (int64_t)hq * P.out.head + d0;
+      *reinterpret_cast<uint4*>(out) = w;
+      if (P.lse && d0 == 0)
+        P.lse[(int64_t)(r.tok0 + tok) * P.Hq + hq] = log_sum(log_top, l, none, P.sink, hq);
+    }
   }
 }
 
@@ -1040,8 +1181,16 @@ cudaError_t launch(const KvAttnParams& P, const CUtensorMap& q, const CUtensorMa
   kv_attn_kernel<D, F16, SPARSE><<<grid, NTHREADS, smem, st>>>(P, q, k, v);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  kv_merge_kernel<D, F16><<<dim3(grid, 4), 256, 0, st>>>(P, grid);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 8, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, F16>, P, grid);
 }
 
 }  // namespace
