@@ -115,16 +115,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// MMA whose A operand (P) is read from tensor memory: M = 128 rows at lanes
-// 0..127, two 16-bit elements of K a column
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -304,6 +294,7 @@ struct Kernel {
   using C = Cfg<D, SPARSE>;
   static constexpr int NST = C::kStages;
   static constexpr int TM_S = 0, TM_O = 2 * NK;          // TMEM columns: S0 S1 O0 O1
+  // all of tensor memory, so its allocation starts at column 0
   static constexpr int kCols = 512;
 
   // -------------------------------------------------------------- loads
@@ -625,91 +616,124 @@ struct Kernel {
   }
 
   // -------------------------------------------------------------- MMA issue
-  static __device__ void issue(const KvAttnParams& P, S& s, uint32_t tmem) {
+  // The tensor-core instructions take their descriptors from the warp's uniform
+  // registers, so this warp stays together: every value below is the same in all
+  // lanes (what comes from shared memory passes through a warp reduction, which
+  // tells the compiler so), no branch divides it, and only the instructions
+  // themselves are predicated on one lane.  (One lane's branch around them: 122
+  // cycles an MMA, and the issue was what bounded the kernel.)
+  static __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+  static __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                                uint32_t accumulate, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+        : "memory");
+  }
+  // A (P) from tensor memory: M = 128 rows at lanes 0..127, two 16-bit elements of K a column
+  static __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                                uint32_t accumulate, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+        : "memory");
+  }
+  static __device__ __forceinline__ void commit(uint64_t* bar, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(on)
+        : "memory");
+  }
+
+  static __device__ void issue(const KvAttnParams& P, S& s) {
     const int lane = threadIdx.x & 31;
+    const uint32_t on = lane == 0;
     uint32_t* status = P.b.status;
-    const uint64_t k_bits = smem_desc_bits(16, 1024, 2);             // K-major, 128B swizzle
-    const uint64_t v_bits = smem_desc_bits(MROWS * 128, 1024, 2);    // MN-major, 128B swizzle
-    const uint32_t fmt = F16 ? 0 : 1;
-    const uint32_t id_qk = idesc_f(fmt, fmt, MROWS, NK, false, false);
-    const uint32_t id_pv = idesc_f(fmt, fmt, MROWS, D, false, true);
-    int base = 0, items = 0, np[2] = {0, 0};
+    constexpr uint64_t k_bits = smem_desc_bits(16, 1024, 2);             // K-major, 128B swizzle
+    constexpr uint64_t v_bits = smem_desc_bits(MROWS * 128, 1024, 2);    // MN-major, 128B swizzle
+    constexpr uint32_t fmt = F16 ? 0 : 1;
+    constexpr uint32_t id_qk = idesc_f(fmt, fmt, MROWS, NK, false, false);
+    constexpr uint32_t id_pv = idesc_f(fmt, fmt, MROWS, D, false, true);
+    const uint32_t q_at = smem_u32(s.q) >> 4, kv_at = smem_u32(s.kv) >> 4;
+    int base = 0, items = 0, np[2] = {0, 0}, pend[2] = {-1, -1};
     uint32_t acc[2] = {0, 0};
     auto wait_tile = [&](int i) { return mbar_wait_warp(&s.full[i % NST], (i / NST) & 1, status, 3); };
     auto qk = [&](int slot, int qslot, int tile) {
       tc_fence_after();
-      if (lane == 0) {
-        const uint64_t a = smem_desc(s.q[qslot], k_bits), b = smem_desc(s.kv[tile % NST], k_bits);
+      const uint64_t a = k_bits | (q_at + qslot * (C::kTile / 16));
+      const uint64_t b = k_bits | (kv_at + tile % NST * (C::kTile / 16));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          // 64 dims (4 steps of 32 bytes) a swizzled half of 128 rows x 128 bytes
-          const uint32_t off = (kk / 4) * (MROWS * 128 / 16) + (kk % 4) * 2;
-          mma_f16(tmem + TM_S + slot * NK, a + off, b + off, id_qk, kk > 0);
-        }
+      for (int kk = 0; kk < D / 16; ++kk) {
+        // 64 dims (4 steps of 32 bytes) a swizzled half of 128 rows x 128 bytes
+        const uint32_t off = (kk / 4) * (MROWS * 128 / 16) + (kk % 4) * 2;
+        mma_ss(TM_S + slot * NK, a + off, b + off, id_qk, kk > 0, on);
       }
     };
     auto pv = [&](int slot, int tile) {
       tc_fence_after();
-      if (lane == 0) {
-        const uint64_t b = smem_desc(s.kv[tile % NST], v_bits);
+      const uint64_t b = v_bits | (kv_at + tile % NST * (C::kTile / 16));
 #pragma unroll
-        for (int kk = 0; kk < NK / 16; ++kk)      // 16 keys: 8 columns of P, 16 rows x 128 bytes
-          mma_f16_ts(tmem + TM_O + slot * D, tmem + TM_S + slot * NK + 8 * kk, b + 128 * kk, id_pv,
-                     kk > 0 ? 1u : acc[slot]);
-      }
+      for (int kk = 0; kk < NK / 16; ++kk)        // 16 keys: 8 columns of P, 16 rows x 128 bytes
+        mma_ts(TM_O + slot * D, TM_S + slot * NK + 8 * kk, b + 128 * kk, id_pv,
+               kk > 0 ? 1u : acc[slot], on);
       acc[slot] = 1;
     };
-    auto commit = [&](uint64_t* bar) {
-      if (lane == 0) tc_commit(bar);
+    // The slot's scores (or, tile < 0, its piece's O) will be complete: said by
+    // this warp's arrive, with what they are of, and the tensor core's.
+    auto signal = [&](int slot, int tile, int blk, uint32_t mask) {
+      if (lane == 0) {
+        s.step[slot] = Step{tile, blk, mask};
+        mbar_arrive(&s.sready[slot]);
+      }
+      __syncwarp();
+      commit(&s.sready[slot], on);
+    };
+    // the P V still to issue of a slot (pend: its V tile), once P is there
+    auto flush = [&](int slot) -> bool {
+      if (pend[slot] < 0) return true;
+      if (!mbar_wait_warp(&s.pready[slot], np[slot] & 1, status, 6)) return false;
+      ++np[slot];
+      if (!wait_tile(pend[slot])) return false;
+      pv(slot, pend[slot]);
+      pend[slot] = -1;
+      return true;
     };
     bool ok = true;
     for (int pieces = 0; ok; ++pieces) {
       const int pi = pieces & 1;
       if (!mbar_wait_warp(&s.pfull[pi], (pieces >> 1) & 1, status, 4)) break;
-      const int n = s.piece[pi].n, dual = s.piece[pi].dual, first = s.piece[pi].first,
-                last = s.piece[pi].last, end = s.piece[pi].end;
-      __syncwarp();
+      const int n = uniform(s.piece[pi].n), dual = uniform(s.piece[pi].dual),
+                first = uniform(s.piece[pi].first), last = uniform(s.piece[pi].last),
+                end = uniform(s.piece[pi].end);
       if (lane == 0) mbar_arrive(&s.pempty[pi]);
+      __syncwarp();
       if (end) break;
       if (first) {
         acc[0] = acc[1] = 0;
         if (!mbar_wait_warp(&s.qfull, items & 1, status, 5)) break;
         ++items;
       }
-      // The slot's scores (or, tile < 0, its piece's O) will be complete: said by
-      // this thread's arrive, with what they are of, and the tensor core's.
-      auto signal = [&](int slot, int tile, int blk, uint32_t mask) {
-        if (lane == 0) {
-          s.step[slot] = Step{tile, blk, mask};
-          mbar_arrive(&s.sready[slot]);
-          tc_commit(&s.sready[slot]);
-        }
-      };
-      int pend[2] = {-1, -1};                              // V tile of the P V still to issue
-      auto flush = [&](int slot) -> bool {
-        if (pend[slot] < 0) return true;
-        if (!mbar_wait_warp(&s.pready[slot], np[slot] & 1, status, 6)) return false;
-        ++np[slot];
-        if (!wait_tile(pend[slot])) return false;
-        pv(slot, pend[slot]);
-        pend[slot] = -1;
-        return true;
-      };
+      pend[0] = pend[1] = -1;
       const uint32_t tile_bits = (1u << min(P.tt, 31)) - 1;
-      for (int i = 0; ok && i < n; ++i) {
-        const int kt = base + 2 * i, vt = kt + 1, mi = (kt >> 1) % kMeta;
-        if (dual) {
+      // block i's K at tile base + 2 i, its V at base + 2 i + 1
+      if (dual) {
+        for (int i = 0; ok && i < n; ++i) {
+          const int kt = base + 2 * i, vt = kt + 1, mi = (kt >> 1) % kMeta;
           int blk = 0;
           uint32_t mask = 0;
 #pragma unroll
           for (int slot = 0; slot < 2; ++slot) {
-            if (!(ok = flush(slot))) break;
+            if (!(ok = ok && flush(slot))) break;
             if (slot == 0) {
               if (!(ok = wait_tile(kt))) break;
               blk = s.blk[mi];
-              mask = s.mask[mi];
+              mask = SPARSE ? (uint32_t)uniform((int)s.mask[mi]) : 0xffffffffu;
             } else if (i > 0) {
-              commit(&s.empty[(vt - 2) % NST]);            // both slots' P V of the block before
+              commit(&s.empty[(vt - 2) % NST], on);        // both slots' P V of the block before
             }
             if (!SPARSE || ((mask >> (slot * P.tt)) & tile_bits)) {
               qk(slot, slot, kt);
@@ -717,34 +741,51 @@ struct Kernel {
               pend[slot] = vt;
             }
           }
-          if (ok) commit(&s.empty[kt % NST]);
-        } else {
-          const int slot = i & 1;
-          if (!(ok = flush(slot))) break;
-          if (i > 1) commit(&s.empty[(vt - 4) % NST]);
-          if (!(ok = wait_tile(kt))) break;
-          qk(slot, 0, kt);
-          commit(&s.empty[kt % NST]);
-          signal(slot, vt, s.blk[mi], s.mask[mi]);
-          pend[slot] = vt;
+          if (ok) commit(&s.empty[kt % NST], on);
         }
+        ok = ok && flush(0);
+        if (ok) signal(0, -1, 0, 0);
+        ok = ok && flush(1);
+        if (ok) signal(1, -1, 0, 0);
+        if (ok && n > 0) commit(&s.empty[(base + 2 * n - 1) % NST], on);
+      } else {
+        for (int i = 0; ok && i < n; i += 2) {
+#pragma unroll
+          for (int slot = 0; slot < 2; ++slot) {
+            if (i + slot < n) {
+              const int kt = base + 2 * (i + slot), vt = kt + 1, mi = (kt >> 1) % kMeta;
+              if (!(ok = ok && flush(slot))) break;
+              if (i > 0) commit(&s.empty[(vt - 4) % NST], on);
+              if (!(ok = wait_tile(kt))) break;
+              qk(slot, 0, kt);
+              commit(&s.empty[kt % NST], on);
+              signal(slot, vt, s.blk[mi], SPARSE ? s.mask[mi] : 0xffffffffu);
+              pend[slot] = vt;
+            }
+          }
+        }
+        const int vt = base + 2 * n - 1;                   // the last block's V tile
+        if (n & 1) {                                       // the older block first: slot 1's
+          ok = ok && flush(1);
+          if (ok) signal(1, -1, 0, 0);
+          if (ok && n > 1) commit(&s.empty[(vt - 2) % NST], on);
+          ok = ok && flush(0);
+          if (ok) signal(0, -1, 0, 0);
+        } else {
+          ok = ok && flush(0);
+          if (ok) signal(0, -1, 0, 0);
+          if (ok && n > 1) commit(&s.empty[(vt - 2) % NST], on);
+          ok = ok && flush(1);
+          if (ok) signal(1, -1, 0, 0);
+        }
+        if (ok && n > 0) commit(&s.empty[vt % NST], on);
       }
-      for (int j = 0; ok && j < 2; ++j) {                  // the older block first
-        const int slot = dual ? j : (n + j) & 1;
-        ok = flush(slot);
-        if (!ok) break;
-        signal(slot, -1, 0, 0);
-        if (!dual && n + j >= 2) commit(&s.empty[(base + 2 * (n + j - 2) + 1) % NST]);
-      }
-      if (ok && dual && n > 0) commit(&s.empty[(base + 2 * n - 1) % NST]);
       if (!ok) break;
-      if (last) commit(&s.qempty);
+      if (last) commit(&s.qempty, on);
       base += 2 * n;
     }
-    if (lane == 0) {
-      tc_commit(&s.done);
-      mbar_wait(&s.done, 0);                               // time bound only
-    }
+    commit(&s.done, on);
+    if (lane == 0) mbar_wait(&s.done, 0);                  // time bound only
     __syncwarp();
   }
 
@@ -783,12 +824,12 @@ struct Kernel {
     return a + b;
   }
 
-  static __device__ void softmax(const KvAttnParams& P, S& s, uint32_t tmem) {
+  static __device__ void softmax(const KvAttnParams& P, S& s) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slot = warp >> 2, r = (warp & 3) * 32 + lane;
     uint32_t* status = P.b.status;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + TM_S + slot * NK, t_o = tmem + lanes + TM_O + slot * D;
+    const uint32_t t_s = lanes + TM_S + slot * NK, t_o = lanes + TM_O + slot * D;
     const float sl2 = P.scale * kLog2e;
     const float grow = kGrow / sl2;
     const int rt = r / P.g, rh = r - rt * P.g;               // token and head of this row
@@ -1037,23 +1078,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s.tmem_base;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up
   if (warp >= 8) {
     regs_down<kOtherRegs>();
     if (warp == 9)
       K::produce(P, s, &tm_q, &tm_k, &tm_v);
     else if (warp == 8)
-      K::issue(P, s, tmem);
+      K::issue(P, s);
   } else {
     regs_up<kSoftmaxRegs>();
-    K::softmax(P, s, tmem);
+    K::softmax(P, s);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {
     tc_fence_after();
-    tmem_dealloc(tmem, K::kCols);
+    tmem_dealloc(0, K::kCols);
   }
 }
 
