@@ -48,11 +48,6 @@ constexpr int kWindow = 2048;                  // blocks whose selection is join
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.0f;                  // log2 of the growth that rescales O
-// 2^f on [-1/2, 1/2] (see exp2_pair)
-constexpr float kExp0 = 0.999999285f, kExp1 = 0.693121791f, kExp2 = 0.240247443f,
-                kExp3 = 0.0559178591f, kExp4 = 0.00957010221f;
-// of 8 pairs of columns, those whose exponentials the FMA units form
-constexpr uint32_t kEmulated = 0x88;
 // cost of an item besides its blocks, in blocks (Q load, epilogue)
 constexpr int kItemCost = 1;
 // least cost of a CTA's range
@@ -76,7 +71,7 @@ struct Step {
   int blk;           // logical block, -1: not to be seen
   uint32_t mask;     // the item's tokens that take it (sparse)
 };
-constexpr int kMeta = 16;
+constexpr int kMeta = 8;
 
 template <int D, bool SPARSE>
 struct Cfg {
@@ -139,34 +134,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// largest of three, NaN if one is
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-// 2^x of two finite x <= 127 without the SFU: x = n + f, n the nearest integer
-// (adding 1.5 2^23 leaves n in the low mantissa bits), 2^f on [-1/2, 1/2] by a
-// degree-4 polynomial fitted to the least largest relative error (2.4e-6, no
-// bias to speak of), n added to the exponent.  Below 2^-125 the result stays
-// there (a weight that no sum of a row's weights, at least 2^-8, can feel).
-__device__ __forceinline__ void exp2_pair(uint64_t x2, float& y0, float& y1) {
-  const float kMagic = 12582912.0f;
-  float a, b;
-  unpair(x2, a, b);
-  const uint64_t x = pair(fmaxf(a, -125.0f), fmaxf(b, -125.0f));
-  const uint64_t t = add2(x, pair(kMagic, kMagic));
-  const uint64_t n = add2(t, pair(-kMagic, -kMagic));
-  const uint64_t f = fma2(n, pair(-1.0f, -1.0f), x);
-  uint64_t p = fma2(f, pair(kExp4, kExp4), pair(kExp3, kExp3));
-  p = fma2(p, f, pair(kExp2, kExp2));
-  p = fma2(p, f, pair(kExp1, kExp1));
-  p = fma2(p, f, pair(kExp0, kExp0));
-  float p0, p1, t0, t1;
-  unpair(p, p0, p1);
-  unpair(t, t0, t1);
-  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
-  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
 template <bool F16>
 __device__ __forceinline__ uint32_t pack16(float x, float y) {
@@ -621,7 +592,7 @@ struct Kernel {
   // lanes (what comes from shared memory passes through a warp reduction, which
   // tells the compiler so), no branch divides it, and only the instructions
   // themselves are predicated on one lane.  (One lane's branch around them: 122
-  // cycles an MMA, and the issue was what bounded the kernel.)
+  // cycles an MMA; so: 71.)
   static __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
   static __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                                 uint32_t accumulate, uint32_t on) {
@@ -682,22 +653,34 @@ struct Kernel {
                kk > 0 ? 1u : acc[slot], on);
       acc[slot] = 1;
     };
-    // The slot's scores (or, tile < 0, its piece's O) will be complete: said by
-    // this warp's arrive, with what they are of, and the tensor core's.
-    auto signal = [&](int slot, int tile, int blk, uint32_t mask) {
+    // A slot's warps answer each step on pready: with P, or, where there were no
+    // scores, that they have read the step (open: the answer is outstanding).
+    bool open[2] = {false, false};
+    auto answered = [&](int slot) -> bool {
+      if (!open[slot]) return true;
+      open[slot] = false;
+      ++np[slot];
+      return mbar_wait_warp(&s.pready[slot], (np[slot] - 1) & 1, status, 6);
+    };
+    // What the scores just issued are of (tile < 0: the piece's O is what comes).
+    // The warps wait for this arrive and for the tensor core's.
+    auto signal = [&](int slot, int tile, int blk, uint32_t mask) -> bool {
+      if (!answered(slot)) return false;
       if (lane == 0) {
         s.step[slot] = Step{tile, blk, mask};
         mbar_arrive(&s.sready[slot]);
       }
       __syncwarp();
       commit(&s.sready[slot], on);
+      open[slot] = true;
+      return true;
     };
-    // the P V still to issue of a slot (pend: its V tile), once P is there
-    auto flush = [&](int slot) -> bool {
+    // the P V still to issue of a slot (pend: its V tile), once P is there; V:
+    // whether the tile is known to have landed
+    auto flush = [&](int slot, bool landed) -> bool {
       if (pend[slot] < 0) return true;
-      if (!mbar_wait_warp(&s.pready[slot], np[slot] & 1, status, 6)) return false;
-      ++np[slot];
-      if (!wait_tile(pend[slot])) return false;
+      if (!answered(slot)) return false;
+      if (!landed && !wait_tile(pend[slot])) return false;
       pv(slot, pend[slot]);
       pend[slot] = -1;
       return true;
@@ -719,66 +702,56 @@ struct Kernel {
       }
       pend[0] = pend[1] = -1;
       const uint32_t tile_bits = (1u << min(P.tt, 31)) - 1;
-      // block i's K at tile base + 2 i, its V at base + 2 i + 1
+      // Block i's K at tile base + 2 i, its V at base + 2 i + 1.  A slot's step: the
+      // P V of its block before, then the Q K^T of its next; past the last block
+      // the P V alone, and word that O is complete.
       if (dual) {
-        for (int i = 0; ok && i < n; ++i) {
-          const int kt = base + 2 * i, vt = kt + 1, mi = (kt >> 1) % kMeta;
+        for (int i = 0; ok && i <= n; ++i) {
+          const int kt = base + 2 * i, mi = (kt >> 1) % kMeta;
           int blk = 0;
           uint32_t mask = 0;
+          const bool both = !SPARSE || (pend[0] >= 0 && pend[1] >= 0);
 #pragma unroll
           for (int slot = 0; slot < 2; ++slot) {
-            if (!(ok = ok && flush(slot))) break;
+            if (!(ok = ok && flush(slot, slot == 1 && both))) break;
+            if (slot == 1 && i > 0) commit(&s.empty[(kt - 1) % NST], on);
+            if (i == n) {
+              ok = signal(slot, -1, 0, 0);
+              continue;
+            }
             if (slot == 0) {
               if (!(ok = wait_tile(kt))) break;
               blk = s.blk[mi];
               mask = SPARSE ? (uint32_t)uniform((int)s.mask[mi]) : 0xffffffffu;
-            } else if (i > 0) {
-              commit(&s.empty[(vt - 2) % NST], on);        // both slots' P V of the block before
             }
             if (!SPARSE || ((mask >> (slot * P.tt)) & tile_bits)) {
               qk(slot, slot, kt);
-              signal(slot, vt, blk, mask);
-              pend[slot] = vt;
+              ok = signal(slot, kt + 1, blk, mask);
+              pend[slot] = kt + 1;
             }
           }
-          if (ok) commit(&s.empty[kt % NST], on);
+          if (ok && i < n) commit(&s.empty[kt % NST], on);
         }
-        ok = ok && flush(0);
-        if (ok) signal(0, -1, 0, 0);
-        ok = ok && flush(1);
-        if (ok) signal(1, -1, 0, 0);
-        if (ok && n > 0) commit(&s.empty[(base + 2 * n - 1) % NST], on);
       } else {
-        for (int i = 0; ok && i < n; i += 2) {
+        for (int i = 0; ok && i < n + 2; i += 2) {         // a slot's first block past n: its end
 #pragma unroll
           for (int slot = 0; slot < 2; ++slot) {
-            if (i + slot < n) {
-              const int kt = base + 2 * (i + slot), vt = kt + 1, mi = (kt >> 1) % kMeta;
-              if (!(ok = ok && flush(slot))) break;
-              if (i > 0) commit(&s.empty[(vt - 4) % NST], on);
-              if (!(ok = wait_tile(kt))) break;
-              qk(slot, 0, kt);
-              commit(&s.empty[kt % NST], on);
-              signal(slot, vt, s.blk[mi], SPARSE ? s.mask[mi] : 0xffffffffu);
-              pend[slot] = vt;
+            const int j = i + slot, kt = base + 2 * j, mi = (kt >> 1) % kMeta;
+            if (!ok || j >= n + 2) break;
+            const bool had = pend[slot] >= 0;
+            if (!(ok = flush(slot, false))) break;
+            if (had) commit(&s.empty[(kt - 3) % NST], on);
+            if (j >= n) {
+              ok = signal(slot, -1, 0, 0);
+              continue;
             }
+            if (!(ok = wait_tile(kt))) break;
+            qk(slot, 0, kt);
+            commit(&s.empty[kt % NST], on);
+            ok = signal(slot, kt + 1, s.blk[mi], SPARSE ? s.mask[mi] : 0xffffffffu);
+            pend[slot] = kt + 1;
           }
         }
-        const int vt = base + 2 * n - 1;                   // the last block's V tile
-        if (n & 1) {                                       // the older block first: slot 1's
-          ok = ok && flush(1);
-          if (ok) signal(1, -1, 0, 0);
-          if (ok && n > 1) commit(&s.empty[(vt - 2) % NST], on);
-          ok = ok && flush(0);
-          if (ok) signal(0, -1, 0, 0);
-        } else {
-          ok = ok && flush(0);
-          if (ok) signal(0, -1, 0, 0);
-          if (ok && n > 1) commit(&s.empty[(vt - 2) % NST], on);
-          ok = ok && flush(1);
-          if (ok) signal(1, -1, 0, 0);
-        }
-        if (ok && n > 0) commit(&s.empty[vt % NST], on);
       }
       if (!ok) break;
       if (last) commit(&s.qempty, on);
@@ -791,7 +764,6 @@ struct Kernel {
 
   // -------------------------------------------------------------- softmax
   // The row's weights 2^(v sl2 - off) to its P columns; returns their sum.
-  template <bool EMULATE>
   static __device__ __forceinline__ float weights(const float* v, float sl2, float off,
                                                   uint32_t t_p, uint32_t kp) {
     const uint64_t scale = pair(sl2, sl2), shift = pair(-off, -off);
@@ -803,13 +775,9 @@ struct Kernel {
       for (int e = 0; e < 32; e += 2) {
         const uint64_t x = fma2(pair(v[c + e], v[c + e + 1]), scale, shift);
         float a, b;
-        if (EMULATE && ((kEmulated >> (e / 2 % 8)) & 1)) {
-          exp2_pair(x, a, b);
-        } else {
-          unpair(x, a, b);
-          a = ex2(a);
-          b = ex2(b);
-        }
+        unpair(x, a, b);
+        a = ex2(a);
+        b = ex2(b);
         if (e & 2)
           s1 = add2(s1, pair(a, b));
         else
@@ -865,7 +833,11 @@ struct Kernel {
         ++ns;
         const Step stp = s.step[slot];
         tc_fence_after();
-        if (stp.tile < 0) break;                             // the last P V is complete
+        if (stp.tile < 0) {                                  // the last P V is complete
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.pready[slot]);
+          break;
+        }
         const int blk = stp.blk, kb = blk * NK;
         if (active) {
           float v[NK];
@@ -885,13 +857,17 @@ struct Kernel {
 #pragma unroll
             for (int c = 0; c < NK; ++c) v[c] = keep && c <= hc && c >= lc ? v[c] : -INFINITY;
           }
-          float x0 = max3(v[0], v[1], v[2]), x1 = max3(v[3], v[4], v[5]);
+          float x[4];
 #pragma unroll
-          for (int c = 6; c < NK - 2; c += 4) {
-            x0 = max3(x0, v[c], v[c + 1]);
-            x1 = max3(x1, v[c + 2], v[c + 3]);
+          for (int c = 0; c < 4; ++c) x[c] = v[c];
+#pragma unroll
+          for (int c = 4; c < NK - 4; c += 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = max3(x[e], v[c + 2 * e], v[c + 2 * e + 1]);
           }
-          float mx = max3(x0, x1, max3(v[NK - 2], v[NK - 1], x0));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] = max3(x[c], v[NK - 4 + c], x[c]);
+          float mx = max3(max3(x[0], x[1], x[2]), x[3], x[3]);
           if (SPARSE && !keep) mx = -INFINITY;
           const bool up = mx > m + grow;
           if (__any_sync(0xffffffffu, up)) {
@@ -913,13 +889,7 @@ struct Kernel {
             }
           }
           const float off = m == -INFINITY ? 0.f : m * sl2;
-          // the SFU gives four exponentials a cycle to an SM quarter and bounds
-          // the whole: part of them are formed by the FMA units, unless a score
-          // is masked, infinite or NaN
-          const uint32_t kp = keep ? 0xffffffffu : 0u;
-          const float sum = edge || __any_sync(0xffffffffu, !(mx <= 3.4e38f))
-                                ? weights<false>(v, sl2, off, t_s, kp)
-                                : weights<true>(v, sl2, off, t_s, kp);
+          const float sum = weights(v, sl2, off, t_s, keep ? 0xffffffffu : 0u);
           l += SPARSE && !keep ? 0.f : sum;
         }
         if (blk >= 0 && (kb + NK > vhi || kb < vlo)) {
@@ -1051,7 +1021,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   using K = Kernel<D, F16, SPARSE>;
   using S = typename K::S;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  S& s = *reinterpret_cast<S*>(smem_raw);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < K::NST; ++i) {
@@ -1208,8 +1178,8 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 template <int D, bool F16, bool SPARSE>
 cudaError_t launch(const KvAttnParams& P, const CUtensorMap& q, const CUtensorMap& k,
                    const CUtensorMap& v, int grid, int dev, cudaStream_t st) {
-  const size_t smem = sizeof(Smem<D, SPARSE>) + 1024;
-  static_assert(sizeof(Smem<D, SPARSE>) + 1024 <= 232448, "shared memory of a CTA");
+  const size_t smem = sizeof(Smem<D, SPARSE>);
+  static_assert(sizeof(Smem<D, SPARSE>) <= 232448, "shared memory of a CTA");
   static unsigned long long configured = 0;
   if (dev >= 64 || !(configured & (1ull << dev))) {
     const cudaError_t e =
