@@ -163,9 +163,23 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The kernels of a call, and calls in a row, are launched while the one before
+// still runs (programmatic dependent launch): no global memory is touched before
+// wait_grid(), which returns when the grid before is complete and flushed.
+__device__ __forceinline__ void wait_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_grid() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- work list
 // Everything below is a function of the lengths alone, so every CTA finds its
 // own range without a word from the others.
+
+// 64-bit quotient; the 32-bit one where that is all it takes (a third of the time)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
 
 struct SeqInfo {
   int q0, n;         // first token row, tokens (0 when its q_start is bad)
@@ -237,23 +251,22 @@ __device__ __forceinline__ SeqInfo shfl_seq(const SeqInfo& s, int src) {
 struct Walk {
   int b0;            // sequences b0 .. b0+31, one a lane
   SeqInfo mine;      // this lane's sequence
-  int64_t cost;      // of all heads of this lane's sequence
+  int64_t head;      // cost of one head of this lane's sequence
   int per_item;
 
   __device__ __forceinline__ void load(const KvAttnParams& P, int first, int lane, bool report) {
     b0 = first;
     mine = SeqInfo{0, 0, 0, 0};
     if (b0 + lane < P.b.B) mine = seq_info(P, b0 + lane, report);
-    cost = 0;
-    if (mine.n > 0 && mine.n <= per_item) cost = item_span(P, mine, 0, mine.n).n + kItemCost;
+    head = 0;
+    if (mine.n > 0 && mine.n <= per_item) head = item_span(P, mine, 0, mine.n).n + kItemCost;
     unsigned many = __ballot_sync(0xffffffffu, mine.n > per_item);
     while (many) {
       const int src = __ffs(many) - 1;
       many &= many - 1;
       const int64_t c = head_cost(P, shfl_seq(mine, src), per_item, lane);
-      if (lane == src) cost = c;
+      if (lane == src) head = c;
     }
-    cost *= P.Hkv;
   }
 };
 
@@ -274,17 +287,18 @@ struct Kernel {
     const int lane = threadIdx.x & 31;
     uint32_t* status = P.b.status;
     const int tt = P.tt, per_item = 2 * tt;
+    wait_grid();
     Walk w;
     w.per_item = per_item;
     int64_t total = 0;
     for (int b0 = 0; b0 < P.b.B; b0 += 32) {
       w.load(P, b0, lane, blockIdx.x == 0);
-      int64_t c = w.cost;
+      int64_t c = w.head * P.Hkv;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
       total += c;
     }
-    int64_t range = (total + gridDim.x - 1) / gridDim.x;
+    int64_t range = quotient(total + gridDim.x - 1, gridDim.x);
     if (range < kMinRange) range = kMinRange;
     const int64_t x0 = range * blockIdx.x, x1 = min(total, x0 + range);
     KvPart* rec = P.parts + 2 * blockIdx.x;
@@ -362,28 +376,29 @@ struct Kernel {
     int64_t at = 0;                    // place of the current group of sequences
     for (int b0 = 0; ok && b0 < P.b.B && at < x1; b0 += 32) {
       if (P.b.B > 32) w.load(P, b0, lane, false);
-      int64_t c = w.cost;
+      const int64_t all = w.head * P.Hkv;
+      int64_t c = all;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xffffffffu, c, o);
         if (lane >= o) c += v;
       }
-      const int64_t end = at + c, begin = end - w.cost;     // this lane's sequence
+      const int64_t end = at + c, begin = end - all;     // this lane's sequence
       const int64_t group_end = __shfl_sync(0xffffffffu, end, 31);
-      unsigned todo = __ballot_sync(0xffffffffu, w.cost > 0 && begin < x1 && end > x0);
+      unsigned todo = __ballot_sync(0xffffffffu, all > 0 && begin < x1 && end > x0);
       while (ok && todo) {
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
         const SeqInfo q = shfl_seq(w.mine, src);
         const int64_t sb = __shfl_sync(0xffffffffu, begin, src);
-        const int64_t hc = __shfl_sync(0xffffffffu, w.cost, src) / P.Hkv;
+        const int64_t hc = __shfl_sync(0xffffffffu, w.head, src);
         const int nit = (q.n + per_item - 1) / per_item;
-        int h = x0 > sb ? (int)((x0 - sb) / hc) : 0;
+        int h = x0 > sb ? (int)quotient(x0 - sb, hc) : 0;
         int64_t hx = sb + h * hc;                            // place of head h's first item
         int k = 0;
         int64_t ix = hx;
         // first item of this head that reaches past x0, 32 at a time
-        if (x0 > hx) {
+        if (x0 > hx && nit > 1) {
           for (;;) {
             int cst = 0;
             if (k + lane < nit)
@@ -621,6 +636,7 @@ struct Kernel {
   }
 
   static __device__ void issue(const KvAttnParams& P, S& s) {
+    wait_grid();
     const int lane = threadIdx.x & 31;
     const uint32_t on = lane == 0;
     uint32_t* status = P.b.status;
@@ -802,6 +818,7 @@ struct Kernel {
     const float grow = kGrow / sl2;
     const int rt = r / P.g, rh = r - rt * P.g;               // token and head of this row
     int ns = 0, no1 = 0;
+    wait_grid();
     float m = -INFINITY, l = 0.f;
     bool has_o = false;
     for (int pieces = 0;; ++pieces) {
@@ -1048,7 +1065,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up
+  next_grid();
   if (warp >= 8) {
     regs_down<kOtherRegs>();
     if (warp == 9)
@@ -1074,7 +1091,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 // parts are small and in L2, so its launch would cost as much as its work.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) kv_merge_kernel(const __grid_constant__ KvAttnParams P, int n_cta) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  next_grid();
+  wait_grid();
   const int c = blockIdx.x;
   const KvPart r = P.parts[2 * c + 1];
   if (r.rows == 0) return;
@@ -1188,18 +1206,21 @@ cudaError_t launch(const KvAttnParams& P, const CUtensorMap& q, const CUtensorMa
     if (e != cudaSuccess) return e;
     if (dev < 64) configured |= 1ull << dev;
   }
-  kv_attn_kernel<D, F16, SPARSE><<<grid, NTHREADS, smem, st>>>(P, q, k, v);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 8, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(NTHREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, F16, SPARSE>, P, q, k, v);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(grid, 8, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, F16>, P, grid);
 }
 
