@@ -49,9 +49,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.0f;                  // log2 of the growth that rescales O
 // cost of an item besides its blocks, in blocks (Q load, epilogue)
-constexpr int kItemCost = 1;
+constexpr int kItemCost = 2;
 // least cost of a CTA's range
-constexpr int kMinRange = 3;
+constexpr int kMinRange = 1;
 
 // What a piece (a range of an item's blocks) tells the MMA and softmax warps.
 struct Piece {
@@ -867,12 +867,15 @@ struct Kernel {
             for (int c = 0; c < NK; ++c) v[c] = __uint_as_float(raw[c]);
           }
           // columns lc .. hc are seen; keep: the row's token takes the block
-          const int hc = hi - kb, lc = lo == (int)0x80000000 ? 0 : lo - kb;
           const bool keep = blk >= 0 && (!SPARSE || !valid || ((stp.mask >> tok) & 1));
-          const bool edge = __any_sync(0xffffffffu, blk < 0 || (keep && (hc < NK - 1 || lc > 0)));
-          if (edge) {
+          const int hc = blk < 0 ? -1 : hi - kb, lc = lo == (int)0x80000000 ? 0 : lo - kb;
+          if (__any_sync(0xffffffffu, (keep || blk < 0) && hc < NK - 1)) {
 #pragma unroll
-            for (int c = 0; c < NK; ++c) v[c] = keep && c <= hc && c >= lc ? v[c] : -INFINITY;
+            for (int c = 0; c < NK; ++c) v[c] = c <= hc ? v[c] : -INFINITY;
+          }
+          if (!SPARSE && __any_sync(0xffffffffu, lc > 0)) {
+#pragma unroll
+            for (int c = 0; c < NK; ++c) v[c] = c >= lc ? v[c] : -INFINITY;
           }
           float x[4];
 #pragma unroll
