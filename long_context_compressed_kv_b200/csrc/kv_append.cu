@@ -14,6 +14,7 @@ namespace v4a {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 3;             // units a thread holds: 80 rows of 128 values in one go
 
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -30,38 +31,76 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Rotate pairs k0 .. k0+7: `a`, `b` are 8 values each; ADJ: the pairs are
-// adjacent within the 16 values, else a holds the first, b the second members.
-template <bool F16, bool ADJ>
-__device__ __forceinline__ void rotate16(uint4& a, uint4& b, const float2* cs) {
-  uint32_t* w[2] = {reinterpret_cast<uint32_t*>(&a), reinterpret_cast<uint32_t*>(&b)};
-  if (ADJ) {
+// Rotate four adjacent pairs by the angles cs[0..3].
+template <bool F16>
+__device__ __forceinline__ void rotate_adjacent(uint4& a, const float2* cs) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&a);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t& x = w[i >> 2][i & 3];
-      const float2 v = unpack2<F16>(x), c = cs[i];
-      x = pack2<F16>(v.x * c.x - v.y * c.y, v.x * c.y + v.y * c.x);
-    }
-  } else {
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack2<F16>(w[i]), c = cs[i];
+    w[i] = pack2<F16>(v.x * c.x - v.y * c.y, v.x * c.y + v.y * c.x);
+  }
+}
+// Rotate eight pairs, a their first members, b their second.
+template <bool F16>
+__device__ __forceinline__ void rotate_halves(uint4& a, uint4& b, const float2* cs) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(&a);
+  uint32_t* w = reinterpret_cast<uint32_t*>(&b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = unpack2<F16>(w[0][i]), y = unpack2<F16>(w[1][i]);
-      const float2 c = cs[2 * i], e = cs[2 * i + 1];
-      w[0][i] = pack2<F16>(x.x * c.x - y.x * c.y, x.y * e.x - y.y * e.y);
-      w[1][i] = pack2<F16>(x.x * c.y + y.x * c.x, x.y * e.y + y.y * e.x);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack2<F16>(u[i]), y = unpack2<F16>(w[i]);
+    const float2 c = cs[2 * i], e = cs[2 * i + 1];
+    u[i] = pack2<F16>(x.x * c.x - y.x * c.y, x.y * e.x - y.y * e.y);
+    w[i] = pack2<F16>(x.x * c.y + y.x * c.x, x.y * e.y + y.y * e.x);
   }
 }
 
 }  // namespace
 
 // One CTA per token; a thread moves 16 values (two 16-byte vectors) of a row
-// at a time: 16 consecutive ones, or, where the pairs lie half of d_rope
-// apart, 8 and their 8 partners.
+// at a time, half the row apart, or, where that is how the pairs lie, half of
+// d_rope: so the lanes' vectors are next to each other in every access.  The rows' addresses need only the token, so a
+// thread's first kBatch units are on their way before its sequence, position
+// and table entry (three dependent loads) and the angles are known.
 template <bool F16>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ KvAppendParams P) {
   __shared__ float2 cs[64];
   const int t = blockIdx.x, tid = threadIdx.x;
+  const int lu = P.d == 128 ? 3 : 2, units = 1 << lu;      // units of 16 values in a row
+  const int keep = (P.d - P.d_rope) / 16, half = P.d_rope / 2;
+  const int hq = P.q.p ? P.Hq : 0;
+  const int n = (hq + 2 * P.Hkv) * units;
+  // unit i: its row, and its two vectors' places in the row
+  auto place = [&](int i, int& row, int& o0, int& o1) {
+    row = i >> lu;
+    const int u = i & (units - 1);
+    if (!P.halves) {
+      o0 = 8 * u;
+      o1 = o0 + P.d / 2;
+    } else if (u < keep) {
+      o0 = 8 * u;
+      o1 = o0 + 8 * keep;
+    } else {
+      o0 = 8 * (u + keep);
+      o1 = o0 + half;
+    }
+  };
+  uint4 a[kBatch], c[kBatch];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i >= n) break;
+      int row, o0, o1;
+      place(i, row, o0, o1);
+      const KvRows& r = row < hq ? P.q : row < hq + P.Hkv ? P.k : P.v;
+      const int h = row < hq ? row : row < hq + P.Hkv ? row - hq : row - hq - P.Hkv;
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(r.p) + t * r.tok + h * r.head;
+      a[j] = __ldcs(reinterpret_cast<const uint4*>(src + o0));
+      c[j] = __ldcs(reinterpret_cast<const uint4*>(src + o1));
+    }
+  };
+  load(tid);
   // the token's sequence: the number of sequences that end at or before it
   int b = 0;
   for (int i = 0; i < P.b.B; i += kThreads)
@@ -80,52 +119,46 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   const int32_t blk = P.b.bt[(int64_t)b * P.b.bps + p / kKvBlock];
   const bool page = blk >= 0 && blk < P.b.n_blocks;
   if (!page && tid == 0) flag(P.b.status, ST_BAD_INDEX);
-  const int half = P.d_rope / 2;
   if (tid < half) {
     // turns in double, reduced to half a turn either way before going to float
     double r = (double)p * P.freq[tid];
     r -= rint(r);
-    float c, s;
-    sincospif(2.0f * (float)r, &s, &c);
-    cs[tid] = make_float2(c, s);
+    float co, si;
+    sincospif(2.0f * (float)r, &si, &co);
+    cs[tid] = make_float2(co, si);
   }
   __syncthreads();
-  const int units = P.d / 16, keep = (P.d - P.d_rope) / 16;
-  const int hq = P.q.p ? P.Hq : 0;
-  const int n = (hq + 2 * P.Hkv) * units;
-  for (int i = tid; i < n; i += kThreads) {
-    const int row = i / units, u = i - row * units;
-    const uint16_t* src;
-    uint16_t* dst;
-    if (row < hq) {
-      src = reinterpret_cast<const uint16_t*>(P.q.p) + t * P.q.tok + row * P.q.head;
-      dst = reinterpret_cast<uint16_t*>(const_cast<void*>(P.q_out.p)) + t * P.q_out.tok +
-            row * P.q_out.head;
-    } else {
-      if (!page) break;
-      const bool is_v = row >= hq + P.Hkv;
-      const int h = row - hq - (is_v ? P.Hkv : 0);
-      const KvRows& r = is_v ? P.v : P.k;
-      src = reinterpret_cast<const uint16_t*>(r.p) + t * r.tok + h * r.head;
-      dst = reinterpret_cast<uint16_t*>(is_v ? P.v_cache : P.k_cache) +
-            (((int64_t)blk * P.Hkv + h) * kKvBlock + p % kKvBlock) * P.d;
+  for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
+    if (i0 != tid) load(i0);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i >= n) break;
+      int row, o0, o1;
+      place(i, row, o0, o1);
+      uint16_t* dst;
+      if (row < hq) {
+        dst = reinterpret_cast<uint16_t*>(const_cast<void*>(P.q_out.p)) + t * P.q_out.tok +
+              row * P.q_out.head;
+      } else {
+        if (!page) break;
+        const bool is_v = row >= hq + P.Hkv;
+        const int h = row - hq - (is_v ? P.Hkv : 0);
+        dst = reinterpret_cast<uint16_t*>(is_v ? P.v_cache : P.k_cache) +
+              (((int64_t)blk * P.Hkv + h) * kKvBlock + p % kKvBlock) * P.d;
+      }
+      if (row < hq + P.Hkv) {
+        const int off = 16 * keep;                           // first rotated dim
+        if (!P.halves) {
+          if (o0 >= off) rotate_adjacent<F16>(a[j], cs + (o0 - off) / 2);
+          if (o1 >= off) rotate_adjacent<F16>(c[j], cs + (o1 - off) / 2);
+        } else if (o0 >= off) {
+          rotate_halves<F16>(a[j], c[j], cs + (o0 - off));
+        }
+      }
+      *reinterpret_cast<uint4*>(dst + o0) = a[j];
+      *reinterpret_cast<uint4*>(dst + o1) = c[j];
     }
-    const bool turn = row < hq + P.Hkv && u >= keep;
-    int o0 = 16 * u, o1 = 16 * u + 8;
-    if (turn && P.halves) {
-      o0 = 16 * keep + 8 * (u - keep);
-      o1 = o0 + half;
-    }
-    uint4 a = *reinterpret_cast<const uint4*>(src + o0);
-    uint4 c = *reinterpret_cast<const uint4*>(src + o1);
-    if (turn) {
-      if (P.halves)
-        rotate16<F16, false>(a, c, cs + 8 * (u - keep));
-      else
-        rotate16<F16, true>(a, c, cs + 8 * (u - keep));
-    }
-    *reinterpret_cast<uint4*>(dst + o0) = a;
-    *reinterpret_cast<uint4*>(dst + o1) = c;
   }
 }
 
