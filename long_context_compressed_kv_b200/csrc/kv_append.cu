@@ -13,9 +13,6 @@ namespace v4a {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kBatch = 3;             // units a thread holds: 80 rows of 128 values in one go
-
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
   if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -60,10 +57,10 @@ __device__ __forceinline__ void rotate_halves(uint4& a, uint4& b, const float2* 
 // One CTA per token; a thread moves 16 values (two 16-byte vectors) of a row
 // at a time, half the row apart, or, where that is how the pairs lie, half of
 // d_rope: so the lanes' vectors are next to each other in every access.  The rows' addresses need only the token, so a
-// thread's first kBatch units are on their way before its sequence, position
+// thread's first NB units are on their way before its sequence, position
 // and table entry (three dependent loads) and the angles are known.
-template <bool F16>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ KvAppendParams P) {
+template <bool F16, int NT, int NB>
+__global__ void __launch_bounds__(NT) kv_append_kernel(const __grid_constant__ KvAppendParams P) {
   __shared__ float2 cs[64];
   const int t = blockIdx.x, tid = threadIdx.x;
   const int lu = P.d == 128 ? 3 : 2, units = 1 << lu;      // units of 16 values in a row
@@ -85,11 +82,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
       o1 = o0 + half;
     }
   };
-  uint4 a[kBatch], c[kBatch];
+  uint4 a[NB], c[NB];
   auto load = [&](int i0) {
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = i0 + j * kThreads;
+    for (int j = 0; j < NB; ++j) {
+      const int i = i0 + j * NT;
       if (i >= n) break;
       int row, o0, o1;
       place(i, row, o0, o1);
@@ -103,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   load(tid);
   // the token's sequence: the number of sequences that end at or before it
   int b = 0;
-  for (int i = 0; i < P.b.B; i += kThreads)
+  for (int i = 0; i < P.b.B; i += NT)
     b += __syncthreads_count(i + tid < P.b.B && P.b.q_start[i + tid + 1] <= t);
   if (b >= P.b.B) return;
   const int q0 = P.b.q_start[b], q1 = P.b.q_start[b + 1];
@@ -128,11 +125,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     cs[tid] = make_float2(co, si);
   }
   __syncthreads();
-  for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
+  for (int i0 = tid; i0 < n; i0 += NB * NT) {
     if (i0 != tid) load(i0);
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = i0 + j * kThreads;
+    for (int j = 0; j < NB; ++j) {
+      const int i = i0 + j * NT;
       if (i >= n) break;
       int row, o0, o1;
       place(i, row, o0, o1);
@@ -162,11 +159,25 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   }
 }
 
-cudaError_t launch_kv_append(const KvAppendParams& P, cudaStream_t st) {
+namespace {
+template <int NT, int NB>
+void launch(const KvAppendParams& P, cudaStream_t st) {
   if (P.f16)
-    kv_append_kernel<true><<<P.b.T, kThreads, 0, st>>>(P);
+    kv_append_kernel<true, NT, NB><<<P.b.T, NT, 0, st>>>(P);
   else
-    kv_append_kernel<false><<<P.b.T, kThreads, 0, st>>>(P);
+    kv_append_kernel<false, NT, NB><<<P.b.T, NT, 0, st>>>(P);
+}
+}  // namespace
+
+cudaError_t launch_kv_append(const KvAppendParams& P, cudaStream_t st) {
+  // Threads a token by its units: 80 rows of 128 values (640 units) take 53.0 us
+  // for 8192 tokens and 3.2 us for 16 on 320 threads, 55.6 and 4.5 us on 128; 40
+  // rows of 64 (160 units) 5.8 us for 1204 tokens on 320, 3.9 us on 128.
+  const int units = ((P.q.p ? P.Hq : 0) + 2 * P.Hkv) * P.d / 16;
+  if (units > 256)
+    launch<320, 2>(P, st);
+  else
+    launch<128, 3>(P, st);
   return cudaGetLastError();
 }
 
