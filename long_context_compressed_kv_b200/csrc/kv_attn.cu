@@ -110,6 +110,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// MMA whose A operand (P) is read from tensor memory: M = 128 rows at lanes
+// 0..127, two 16-bit elements of K a column
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -171,6 +181,11 @@ __device__ __forceinline__ void next_grid() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
 // ---------------------------------------------------------------- work list
 // Everything below is a function of the lengths alone, so every CTA finds its
 // own range without a word from the others.
@@ -603,42 +618,17 @@ struct Kernel {
 
   // -------------------------------------------------------------- MMA issue
   // The tensor-core instructions take their descriptors from the warp's uniform
-  // registers, so this warp stays together: every value below is the same in all
-  // lanes (what comes from shared memory passes through a warp reduction, which
-  // tells the compiler so), no branch divides it, and only the instructions
-  // themselves are predicated on one lane.  (One lane's branch around them: 122
-  // cycles an MMA; so: 71.)
-  static __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
-  static __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                                uint32_t accumulate, uint32_t on) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
-        : "memory");
-  }
-  // A (P) from tensor memory: M = 128 rows at lanes 0..127, two 16-bit elements of K a column
-  static __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                                uint32_t accumulate, uint32_t on) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
-        : "memory");
-  }
-  static __device__ __forceinline__ void commit(uint64_t* bar, uint32_t on) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-            smem_u32(bar)),
-        "r"(on)
-        : "memory");
-  }
-
+  // registers.  The lane that elect.sync names runs this alone: the compiler then
+  // knows the branch for one lane's, and its values for uniform ones.  (A branch
+  // on lane == 0: 122 cycles an MMA; the whole warp together, the instructions
+  // predicated on one lane and every wait taken by all: 71, but 5% more time in
+  // all than this.)
   static __device__ void issue(const KvAttnParams& P, S& s) {
     wait_grid();
-    const int lane = threadIdx.x & 31;
-    const uint32_t on = lane == 0;
+    if (elect_one()) issue_one(P, s);
+    __syncwarp();
+  }
+  static __device__ __forceinline__ void issue_one(const KvAttnParams& P, S& s) {
     uint32_t* status = P.b.status;
     constexpr uint64_t k_bits = smem_desc_bits(16, 1024, 2);             // K-major, 128B swizzle
     constexpr uint64_t v_bits = smem_desc_bits(MROWS * 128, 1024, 2);    // MN-major, 128B swizzle
@@ -648,7 +638,7 @@ struct Kernel {
     const uint32_t q_at = smem_u32(s.q) >> 4, kv_at = smem_u32(s.kv) >> 4;
     int base = 0, items = 0, np[2] = {0, 0}, pend[2] = {-1, -1};
     uint32_t acc[2] = {0, 0};
-    auto wait_tile = [&](int i) { return mbar_wait_warp(&s.full[i % NST], (i / NST) & 1, status, 3); };
+    auto wait_tile = [&](int i) { return mbar_wait_at(&s.full[i % NST], (i / NST) & 1, status, 3); };
     auto qk = [&](int slot, int qslot, int tile) {
       tc_fence_after();
       const uint64_t a = k_bits | (q_at + qslot * (C::kTile / 16));
@@ -657,7 +647,7 @@ struct Kernel {
       for (int kk = 0; kk < D / 16; ++kk) {
         // 64 dims (4 steps of 32 bytes) a swizzled half of 128 rows x 128 bytes
         const uint32_t off = (kk / 4) * (MROWS * 128 / 16) + (kk % 4) * 2;
-        mma_ss(TM_S + slot * NK, a + off, b + off, id_qk, kk > 0, on);
+        mma_f16(TM_S + slot * NK, a + off, b + off, id_qk, kk > 0);
       }
     };
     auto pv = [&](int slot, int tile) {
@@ -665,8 +655,8 @@ struct Kernel {
       const uint64_t b = v_bits | (kv_at + tile % NST * (C::kTile / 16));
 #pragma unroll
       for (int kk = 0; kk < NK / 16; ++kk)        // 16 keys: 8 columns of P, 16 rows x 128 bytes
-        mma_ts(TM_O + slot * D, TM_S + slot * NK + 8 * kk, b + 128 * kk, id_pv,
-               kk > 0 ? 1u : acc[slot], on);
+        mma_f16_ts(TM_O + slot * D, TM_S + slot * NK + 8 * kk, b + 128 * kk, id_pv,
+               kk > 0 ? 1u : acc[slot]);
       acc[slot] = 1;
     };
     // A slot's warps answer each step on pready: with P, or, where there were no
@@ -676,18 +666,15 @@ struct Kernel {
       if (!open[slot]) return true;
       open[slot] = false;
       ++np[slot];
-      return mbar_wait_warp(&s.pready[slot], (np[slot] - 1) & 1, status, 6);
+      return mbar_wait_at(&s.pready[slot], (np[slot] - 1) & 1, status, 6);
     };
     // What the scores just issued are of (tile < 0: the piece's O is what comes).
     // The warps wait for this arrive and for the tensor core's.
     auto signal = [&](int slot, int tile, int blk, uint32_t mask) -> bool {
       if (!answered(slot)) return false;
-      if (lane == 0) {
-        s.step[slot] = Step{tile, blk, mask};
-        mbar_arrive(&s.sready[slot]);
-      }
-      __syncwarp();
-      commit(&s.sready[slot], on);
+      s.step[slot] = Step{tile, blk, mask};
+      mbar_arrive(&s.sready[slot]);
+      tc_commit(&s.sready[slot]);
       open[slot] = true;
       return true;
     };
@@ -704,16 +691,15 @@ struct Kernel {
     bool ok = true;
     for (int pieces = 0; ok; ++pieces) {
       const int pi = pieces & 1;
-      if (!mbar_wait_warp(&s.pfull[pi], (pieces >> 1) & 1, status, 4)) break;
-      const int n = uniform(s.piece[pi].n), dual = uniform(s.piece[pi].dual),
-                first = uniform(s.piece[pi].first), last = uniform(s.piece[pi].last),
-                end = uniform(s.piece[pi].end);
-      if (lane == 0) mbar_arrive(&s.pempty[pi]);
-      __syncwarp();
+      if (!mbar_wait_at(&s.pfull[pi], (pieces >> 1) & 1, status, 4)) break;
+      const int n = s.piece[pi].n, dual = s.piece[pi].dual,
+                first = s.piece[pi].first, last = s.piece[pi].last,
+                end = s.piece[pi].end;
+      mbar_arrive(&s.pempty[pi]);
       if (end) break;
       if (first) {
         acc[0] = acc[1] = 0;
-        if (!mbar_wait_warp(&s.qfull, items & 1, status, 5)) break;
+        if (!mbar_wait_at(&s.qfull, items & 1, status, 5)) break;
         ++items;
       }
       pend[0] = pend[1] = -1;
@@ -730,7 +716,7 @@ struct Kernel {
 #pragma unroll
           for (int slot = 0; slot < 2; ++slot) {
             if (!(ok = ok && flush(slot, slot == 1 && both))) break;
-            if (slot == 1 && i > 0) commit(&s.empty[(kt - 1) % NST], on);
+            if (slot == 1 && i > 0) tc_commit(&s.empty[(kt - 1) % NST]);
             if (i == n) {
               ok = signal(slot, -1, 0, 0);
               continue;
@@ -738,7 +724,7 @@ struct Kernel {
             if (slot == 0) {
               if (!(ok = wait_tile(kt))) break;
               blk = s.blk[mi];
-              mask = SPARSE ? (uint32_t)uniform((int)s.mask[mi]) : 0xffffffffu;
+              mask = SPARSE ? s.mask[mi] : 0xffffffffu;
             }
             if (!SPARSE || ((mask >> (slot * P.tt)) & tile_bits)) {
               qk(slot, slot, kt);
@@ -746,7 +732,7 @@ struct Kernel {
               pend[slot] = kt + 1;
             }
           }
-          if (ok && i < n) commit(&s.empty[kt % NST], on);
+          if (ok && i < n) tc_commit(&s.empty[kt % NST]);
         }
       } else {
         for (int i = 0; ok && i < n + 2; i += 2) {         // a slot's first block past n: its end
@@ -756,26 +742,25 @@ struct Kernel {
             if (!ok || j >= n + 2) break;
             const bool had = pend[slot] >= 0;
             if (!(ok = flush(slot, false))) break;
-            if (had) commit(&s.empty[(kt - 3) % NST], on);
+            if (had) tc_commit(&s.empty[(kt - 3) % NST]);
             if (j >= n) {
               ok = signal(slot, -1, 0, 0);
               continue;
             }
             if (!(ok = wait_tile(kt))) break;
             qk(slot, 0, kt);
-            commit(&s.empty[kt % NST], on);
+            tc_commit(&s.empty[kt % NST]);
             ok = signal(slot, kt + 1, s.blk[mi], SPARSE ? s.mask[mi] : 0xffffffffu);
             pend[slot] = kt + 1;
           }
         }
       }
       if (!ok) break;
-      if (last) commit(&s.qempty, on);
+      if (last) tc_commit(&s.qempty);
       base += 2 * n;
     }
-    commit(&s.done, on);
-    if (lane == 0) mbar_wait(&s.done, 0);                  // time bound only
-    __syncwarp();
+    tc_commit(&s.done);
+    mbar_wait(&s.done, 0);                                 // time bound only
   }
 
   // -------------------------------------------------------------- softmax
