@@ -1102,14 +1102,15 @@ __global__ void __launch_bounds__(256) kv_merge_kernel(const __grid_constant__ K
   next_grid();
   wait_grid();
   const int c = blockIdx.x;
-  const KvPart r = P.parts[2 * c + 1];
-  if (r.rows == 0) return;
   // the CTA whose first piece ends the item (kKvMaxCtas <= 256 threads look at once)
   __shared__ int last_s;
+  const int cand = c + 1 + threadIdx.x;
+  const int ends = cand < n_cta ? P.parts[2 * cand].ends : 0;
+  const KvPart r = P.parts[2 * c + 1];
+  if (r.rows == 0) return;
   if (threadIdx.x == 0) last_s = n_cta - 1;
   __syncthreads();
-  const int cand = c + 1 + threadIdx.x;
-  if (cand < n_cta && P.parts[2 * cand].ends) atomicMin(&last_s, cand);
+  if (ends) atomicMin(&last_s, cand);
   __syncthreads();
   const int last = last_s;
   // 256 threads: D / 8 to a row's dims, `lanes` to its parts, the rest to rows
@@ -1123,27 +1124,44 @@ __global__ void __launch_bounds__(256) kv_merge_kernel(const __grid_constant__ K
     const int i = min(i0 + rl, r.rows - 1);
     const int tok = i / P.g, hd = i - tok * P.g;
     const int row = tok / P.tt * MROWS + (tok % P.tt) * P.g + hd;
-    auto place = [&](int q) { return (int64_t)(q == c ? 2 * c + 1 : 2 * q) * (2 * MROWS) + row; };
+    // four parts at a time, their loads all on their way before the first is used
     float top = -INFINITY, l = 0.f, x[8] = {};
-    for (int q = c + pl; q <= last; q += lanes) top = fmaxf(top, P.part_ml[place(q)].x);
-    const float off = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-    for (int q = c + pl; q <= last; q += lanes) {
-      const int64_t at = place(q);
-      const float2 ml = P.part_ml[at];
-      const float f = ex2(ml.x - off);
-      const float4 u = *reinterpret_cast<const float4*>(P.part_o + at * D + d0);
-      const float4 v = *reinterpret_cast<const float4*>(P.part_o + at * D + d0 + 4);
-      l += ml.y * f;
-      x[0] += u.x * f;
-      x[1] += u.y * f;
-      x[2] += u.z * f;
-      x[3] += u.w * f;
-      x[4] += v.x * f;
-      x[5] += v.y * f;
-      x[6] += v.z * f;
-      x[7] += v.w * f;
+    for (int q0 = c + pl; q0 <= last; q0 += 4 * lanes) {
+      float2 ml[4];
+      float4 u[4], v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int q = q0 + j * lanes;
+        ml[j] = make_float2(-INFINITY, 0.f);
+        u[j] = v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q <= last) {
+          const int64_t at = (int64_t)(q == c ? 2 * c + 1 : 2 * q) * (2 * MROWS) + row;
+          ml[j] = P.part_ml[at];
+          u[j] = *reinterpret_cast<const float4*>(P.part_o + at * D + d0);
+          v[j] = *reinterpret_cast<const float4*>(P.part_o + at * D + d0 + 4);
+        }
+      }
+      const float t4 = fmaxf(top, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+      const float z = t4 == -INFINITY ? 0.f : t4, f0 = ex2(top - z);
+      top = t4;
+      l *= f0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= f0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float f = ex2(ml[j].x - z);
+        l += ml[j].y * f;
+        x[0] += u[j].x * f;
+        x[1] += u[j].y * f;
+        x[2] += u[j].z * f;
+        x[3] += u[j].w * f;
+        x[4] += v[j].x * f;
+        x[5] += v[j].y * f;
+        x[6] += v[j].z * f;
+        x[7] += v[j].w * f;
+      }
     }
+    const float off = top == -INFINITY ? 0.f : top;
     if (lanes > 1) {                     // the lanes' sums, in the lanes' order
       __syncthreads();
       ts[threadIdx.x] = top;
@@ -1226,7 +1244,7 @@ cudaError_t launch(const KvAttnParams& P, const CUtensorMap& q, const CUtensorMa
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, F16, SPARSE>, P, q, k, v);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(grid, 8, 1);
+  cfg.gridDim = dim3(grid, 16, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, F16>, P, grid);
