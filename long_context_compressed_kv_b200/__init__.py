@@ -270,41 +270,44 @@ def kv_workspace(desc: KvDesc, device="cuda") -> torch.Tensor:
     return ws
 
 
-def _kv_rows(name, t, T, H, d, dtype):
+# A decode step's calls take a few microseconds on the GPU, so what checks and
+# marshals their arguments asks each tensor for as little as it can.
+def _kv_rows(name, t, shape, dtype, dev):
     """(pointer, token stride, head stride) of [T][H][d] rows; their last dim contiguous."""
-    if t.shape != (T, H, d) or t.dtype is not dtype:
-        raise ValueError(f"{name} must be [{T}][{H}][{d}] in {dtype}, got {tuple(t.shape)} in "
-                         f"{t.dtype}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {shape} in {dtype} on cuda:{dev}, got "
+                         f"{tuple(t.shape)} in {t.dtype} on {t.device}")
     tok, head, one = t.stride()
+    T, H, d = shape
     if one != 1 and T:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     # a dimension of one element may have any stride: it is never taken
     return t.data_ptr(), tok if T > 1 else H * d, head if H > 1 else d
 
 
-def _kv_small(name, t, dtype, shape):
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got "
-                         f"{t.dtype} {tuple(t.shape)}")
+def _kv_small(name, t, shape, dtype, dev):
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on "
+                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _kv_common(d, Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table, ws, others):
+def _kv_cache(d, Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table, ws):
     """Checked (device, B, pool and table fields) of a call on a 16-bit K/V layer."""
     dev = k_cache.get_device()
-    if dev < 0:
-        raise ValueError("tensor must live on the GPU")
-    for t in (v_cache, q_start, kv_len, block_table, ws, *others):
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on {t.device} and {k_cache.device} in one call")
-    B = kv_len.shape[0] if kv_len.dim() == 1 else -1
-    pool = (k_cache.shape[0], Hkv, 128, d)
-    bps = block_table.shape[1] if block_table.dim() == 2 else -1
-    return dev, B, (_kv_small("k_cache", k_cache, dtype, pool),
-                    _kv_small("v_cache", v_cache, dtype, pool), pool[0],
-                    _kv_small("q_start", q_start, torch.int32, (B + 1,)),
-                    _kv_small("kv_len", kv_len, torch.int64, (B,)),
-                    _kv_small("block_table", block_table, torch.int32, (B, bps)), bps)
+    if dev < 0 or ws.get_device() != dev:
+        raise ValueError(f"tensors must live on one GPU, got {k_cache.device} and {ws.device}")
+    if kv_len.dim() != 1 or block_table.dim() != 2 or k_cache.dim() != 4:
+        raise ValueError("kv_len is [B], block_table [B][blocks_per_seq], a cache "
+                         "[n_blocks][Hkv][128][d]")
+    n, B, bps = len(k_cache), len(kv_len), block_table.shape[1]
+    pool = (n, Hkv, 128, d)
+    return dev, B, (_kv_small("k_cache", k_cache, pool, dtype, dev),
+                    _kv_small("v_cache", v_cache, pool, dtype, dev), n,
+                    _kv_small("q_start", q_start, (B + 1,), torch.int32, dev),
+                    _kv_small("kv_len", kv_len, (B,), torch.int64, dev),
+                    _kv_small("block_table", block_table, (B, bps), torch.int32, dev), bps)
 
 
 _KV_CALLS = {fn: (_abi.packed_call(fn), fmt.pack) for fn, fmt in _abi.PACKED.items()}
@@ -337,34 +340,35 @@ def kv_append(desc: KvDesc, *, k, v, k_cache, v_cache, q_start, kv_len, block_ta
     included), block_table int32 [B][blocks_per_seq]."""
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    d, Hkv, dtype, T = desc.d, desc.Hkv, _KV_TORCH.get(desc.dtype), k.shape[0]
-    dev, B, cache = _kv_common(d, Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table, ws,
-                               (k, v, q, q_out))
+    d, Hkv, dtype, T = desc.d, desc.Hkv, _KV_TORCH.get(desc.dtype), len(k)
+    dev, B, cache = _kv_cache(d, Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table, ws)
+    kv = (T, Hkv, d)
     if q is None:
         rows = (0, 0, 0, 0, 0, 0)
     else:
-        rows = (*_kv_rows("q", q, T, desc.Hq, d, dtype),
-                *_kv_rows("q_out", q_out, T, desc.Hq, d, dtype))
-    _kv_call("v4attn_kv_append", desc, dev, ws, stream, T, B, *_kv_rows("k", k, T, Hkv, d, dtype),
-             *_kv_rows("v", v, T, Hkv, d, dtype), *rows, *cache)
+        qs = (T, desc.Hq, d)
+        rows = (*_kv_rows("q", q, qs, dtype, dev), *_kv_rows("q_out", q_out, qs, dtype, dev))
+    _kv_call("v4attn_kv_append", desc, dev, ws, stream, T, B, *_kv_rows("k", k, kv, dtype, dev),
+             *_kv_rows("v", v, kv, dtype, dev), *rows, *cache)
 
 
 def _kv_attention(fn, desc, q, k_cache, v_cache, q_start, kv_len, block_table, out, ws, lse, sink,
                   idx, n_local, stream):
-    d, Hq, dtype, T = desc.d, desc.Hq, _KV_TORCH.get(desc.dtype), q.shape[0]
-    dev, B, cache = _kv_common(d, desc.Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table,
-                               ws, (q, out, lse, sink, idx))
+    d, Hq, dtype, T = desc.d, desc.Hq, _KV_TORCH.get(desc.dtype), len(q)
+    dev, B, cache = _kv_cache(d, desc.Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table,
+                              ws)
+    rows = (T, Hq, d)
     n_lists, n_sel = 1, 0
     if idx is not None:
-        n_lists = idx.shape[1] if idx.dim() == 3 else 1
-        n_sel = idx.shape[-1] if idx.dim() else 0
-        idx = _kv_small("idx", idx, torch.int32,
-                        (T, n_lists, n_sel) if idx.dim() == 3 else (T, n_sel))
-    _kv_call(fn, desc, dev, ws, stream, T, B, *_kv_rows("q", q, T, Hq, d, dtype), *cache,
+        if idx.dim() not in (2, 3):
+            raise ValueError("idx must be [T][n_lists][n_sel] or [T][n_sel]")
+        n_lists, n_sel = idx.shape[1] if idx.dim() == 3 else 1, idx.shape[-1]
+        idx = _kv_small("idx", idx, (T, *idx.shape[1:]), torch.int32, dev)
+    _kv_call(fn, desc, dev, ws, stream, T, B, *_kv_rows("q", q, rows, dtype, dev), *cache,
              idx or 0, n_lists, n_sel, n_local,
-             0 if sink is None else _kv_small("sink", sink, torch.float32, (Hq,)),
-             *_kv_rows("out", out, T, Hq, d, dtype),
-             0 if lse is None else _kv_small("lse", lse, torch.float32, (T, Hq)))
+             0 if sink is None else _kv_small("sink", sink, (Hq,), torch.float32, dev),
+             *_kv_rows("out", out, rows, dtype, dev),
+             0 if lse is None else _kv_small("lse", lse, (T, Hq), torch.float32, dev))
 
 
 def paged_attention(desc: KvDesc, *, q, k_cache, v_cache, q_start, kv_len, block_table, out, ws,

@@ -380,17 +380,17 @@ struct Kernel {
       return q_tiles == 0 || ++ahead < 2 || load_q();
     };
     // the pool block of logical block lb (lane-wise); -1 where the table holds none
-    auto page = [&](int b, int lb, bool want) -> int {
-      int pb = -1;
-      if (want) {
-        pb = __ldg(P.b.bt + (int64_t)b * P.b.bps + lb);
-        if (pb < 0 || pb >= P.b.n_blocks) {
-          pb = -1;
-          flag(status, ST_BAD_INDEX);
-        }
+    auto entry = [&](int b, int lb, bool want) -> int {
+      return want ? __ldg(P.b.bt + (int64_t)b * P.b.bps + lb) : -1;
+    };
+    auto checked = [&](int pb, bool want) -> int {
+      if (want && (pb < 0 || pb >= P.b.n_blocks)) {
+        pb = -1;
+        flag(status, ST_BAD_INDEX);
       }
       return pb;
     };
+    auto page = [&](int b, int lb, bool want) -> int { return checked(entry(b, lb, want), want); };
 
     // find the first item of the range
     int64_t at = 0;                    // place of the current group of sequences
@@ -471,13 +471,16 @@ struct Kernel {
             q_tiles = pc.dual + 1;
             q_head = h * P.g;
             q_tok = pc.tok0;
+            // (the first table entries are on their way while Q is asked for)
+            int pb = SPARSE ? 0 : entry(pc.b, sp.lo + e0 + lane, e0 + lane < e1);
             if (items == 0) ok = load_q();
             if (!SPARSE) {
               pc.first = pc.last = 1;
               pc.n = e1 - e0;
               ok = ok && publish(pc);
               for (int e = e0; ok && e < e1; e += 32) {
-                const int pb = page(pc.b, sp.lo + e + lane, e + lane < e1);
+                if (e > e0) pb = entry(pc.b, sp.lo + e + lane, e + lane < e1);
+                pb = checked(pb, e + lane < e1);
                 const int m = min(32, e1 - e);
                 for (int i = 0; ok && i < m; ++i)
                   ok = load_block(h, sp.lo + e + i, __shfl_sync(0xffffffffu, pb, i), 0xffffffffu);
