@@ -585,3 +585,182 @@ def test_nothing_to_do():
     c = Case([0, 0], [200, 0], 8, 2, 64, seed=1, front=2, behind=3)
     out, lse = attend(c)
     assert (out == 7.0).all() and (lse == 7.0).all()
+
+
+# ------------------------------------------------------------------ many sequences, many items
+
+
+@pytest.mark.parametrize("B", [33, 100, 300])
+def test_many_sequences(B):
+    """More sequences than a warp looks at in one go, some without new tokens,
+    some with several, of every length up to 400."""
+    rng = np.random.default_rng(B)
+    ns = rng.choice([0, 1, 1, 1, 2, 9], B).tolist()
+    ls = [int(n + rng.integers(0, 400 - n)) for n in ns]
+    c = Case(ns, ls, 4, 2, 64, seed=B)
+    check(c, *attend(c), reference(c))
+    idx = lists_for(c, 2, 2, seed=B)
+    check(c, *select(c, idx, 1), reference(c, idx=idx, n_local=1))
+
+
+def test_many_items_of_a_head():
+    """128 query heads on one K/V head: two tokens an item, more items of a
+    head than lanes; and the same for a sequence behind it."""
+    c = Case([90, 70], [300, 75], 128, 1, 64, seed=2)
+    check(c, *attend(c), reference(c))
+    idx = lists_for(c, 1, 2, seed=1)
+    check(c, *select(c, idx, 1), reference(c, idx=idx, n_local=1))
+
+
+def test_one_row_over_every_sm():
+    """A single query head on a long history: as many parts as CTAs."""
+    c = Case([1], [40000], 1, 1, 128, seed=5)
+    sink = torch.tensor([1.5])
+    for sk in (None, sink):
+        check(c, *attend(c, sink=sk), reference(c, sink=sk))
+
+
+def test_longest_lists():
+    """2048 entries a list, most of them of no block, and a long last range."""
+    c = Case([1, 3], [5000, 2500], 2, 1, 64, seed=6)
+    idx = torch.full((c.T, 1, 2048), -1, dtype=torch.int32)
+    rng = np.random.default_rng(0)
+    for t, _, p in c.tokens():
+        m = p // BLOCK + 1
+        at = np.sort(rng.permutation(2048)[:m // 2])
+        idx[t, 0, at] = torch.from_numpy(np.sort(rng.permutation(m)[:m // 2]).astype(np.int32))
+    check(c, *select(c, idx, 0), reference(c, idx=idx, n_local=0))
+    check(c, *select(c, idx, 1 << 30), reference(c, idx=idx, n_local=1 << 30))
+
+
+def test_selection_joined_in_windows():
+    """Histories of more than 2048 blocks and so many items that a CTA's range
+    of blocks passes 2048: the joined selection goes on in a second window.
+    One block's K and V serve every table entry, so that only positions and
+    masks tell; sampled tokens against the reference."""
+    v = v4()
+    L, n, Hkv, d, n_sel = 2100 * BLOCK - 37, 640, 8, 64, 5
+    nb = -(-L // BLOCK)
+    g = torch.Generator().manual_seed(4)
+    kb = torch.randn(7, Hkv, BLOCK, d, generator=g).to(torch.float16)
+    vb = torch.randn(7, Hkv, BLOCK, d, generator=g).to(torch.float16)
+    table = torch.randint(0, 7, (1, nb), generator=g, dtype=torch.int32)
+    q = torch.randn(n, Hkv, d, generator=g).to(torch.float16)
+    idx = torch.stack([torch.randperm(nb - 6, generator=g)[:n_sel].sort().values
+                       for _ in range(n)]).to(torch.int32)
+    desc = v.kv_desc(Hkv, Hkv, d, dtype=torch.float16)
+    ws = v.kv_workspace(desc)
+    out = torch.empty(n, Hkv, d, dtype=torch.float16, device="cuda")
+    lse = torch.empty(n, Hkv, device="cuda")
+    v.block_sparse_attention(
+        desc, q=q.cuda(), k_cache=kb.cuda(), v_cache=vb.cuda(), out=out, lse=lse, ws=ws,
+        q_start=torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+        kv_len=torch.tensor([L], dtype=torch.int64, device="cuda"), block_table=table.cuda(),
+        idx=idx.cuda(), n_local=2)
+    assert v.device_status(ws) == 0
+    u = 2.0 ** -11
+    for t in list(range(0, n, 37)) + [n - 1]:
+        p = L - n + t
+        last = p // BLOCK
+        blocks = sorted(set(idx[t].tolist()) | {last - 1, last})
+        k = torch.cat([kb[table[0, b]][:, :(p % BLOCK + 1 if b == last else BLOCK)]
+                       for b in blocks], 1).double()
+        x = torch.cat([vb[table[0, b]][:, :(p % BLOCK + 1 if b == last else BLOCK)]
+                       for b in blocks], 1).double()
+        s = (k @ q[t].double()[:, :, None])[..., 0] / math.sqrt(d)
+        w = s.softmax(1)
+        want = (w[:, None] @ x)[:, 0]
+        e = d * 2.0 ** -23 * (k.abs() @ q[t].double().abs()[:, :, None]).amax(1) / math.sqrt(d)
+        tol = u * want.abs() + (u + 2 * (e + 2.0 ** -18)) * (w[:, None] @ x.abs())[:, 0] * (1 + u)
+        assert ((out[t].double().cpu() - want).abs() <= tol).all(), t
+        z = s.logsumexp(1)
+        assert ((lse[t].double().cpu() - z).abs() <= e[:, 0] + 2.0 ** -18 + 2.0 ** -21 * 10).all()
+
+
+def test_head_major_queries():
+    """q stored [Hq][T][d] and handed over transposed: head stride above token stride."""
+    v = v4()
+    c = Case([20, 3], [300, 200], 8, 2, 128, seed=9)
+    desc = desc_of(c)
+    ws = v.kv_workspace(desc)
+    q = c.q.transpose(0, 1).contiguous().cuda().transpose(0, 1)
+    out, lse = outputs(c)
+    v.paged_attention(desc, q=q, out=out, lse=lse, **c.args(ws))
+    check(c, out, lse, reference(c))
+
+
+def test_without_lse_and_with_shared_blocks():
+    """Two sequences whose first blocks are the same pool blocks (a shared
+    prefix); no lse asked for."""
+    v = v4()
+    c = Case([2, 1], [400, 300], 8, 2, 128, seed=13)
+    for hist in (c.hist_k, c.hist_v):
+        hist[1][:256] = hist[0][:256]
+    c.table[1, :2] = c.table[0, :2]
+    desc = desc_of(c)
+    ws = v.kv_workspace(desc)
+    out, lse = outputs(c)
+    v.paged_attention(desc, q=c.q.cuda(), out=out, **c.args(ws))
+    ref = reference(c)
+    full = attend(c)
+    check(c, *full, ref)
+    assert torch.equal(out, full[0]) and (lse == 7.0).all()
+
+
+def test_a_visible_nan_shows():
+    """A NaN key or value that a query sees is not swallowed."""
+    c = Case([1], [700], 8, 2, 128, seed=14)
+    c.k_pool[c.table[0, 3], 1, 5] = math.nan
+    out, lse = attend(c)
+    assert out[:, 4:].isnan().all() and lse[:, 4:].isnan().all()
+    assert out[:, :4].isfinite().all()
+    c = Case([1], [700], 8, 2, 128, seed=14)
+    c.v_pool[c.table[0, 3], 0, 5, 7] = math.nan
+    out, lse = attend(c)
+    assert out[:, :4, 7].isnan().all() and lse.isfinite().all()
+
+
+def test_calls_in_a_row_on_one_stream():
+    """Append, attend, select and again on one workspace without a pause: each
+    reads what the one before wrote."""
+    v = v4()
+    c = Case([1, 1], [300, 1], 8, 2, 64, "fp16", seed=15, bps=4, spare=4)
+    c.table = np.arange(8, dtype=np.int32).reshape(2, 4)
+    c.n_blocks = 8
+    desc = desc_of(c, d_rope=0)
+    ws = v.kv_workspace(desc)
+    steps, lens = 60, [100, 0]
+    g = torch.Generator().manual_seed(1)
+    qs, ks, xs = (torch.randn(steps, 2, h, 64, generator=g).half() for h in (8, 2, 2))
+    first = torch.randn(2, 100, 2, 64, generator=g).half()
+    kc = torch.full((8, 2, BLOCK, 64), math.nan, dtype=torch.float16)
+    vc = kc.clone()
+    kc[0, :, :100], vc[0, :, :100] = first[0].transpose(0, 1), first[1].transpose(0, 1)
+    kc, vc = kc.cuda(), vc.cuda()
+    dev = [t.cuda() for t in (qs, ks, xs)]
+    kv_len = torch.tensor(lens, dtype=torch.int64, device="cuda")
+    outs = torch.empty(steps, 2, 2, 8, 64, dtype=torch.float16, device="cuda")
+    idx = torch.tensor([[0, -1], [0, -1]], dtype=torch.int32, device="cuda")
+    q_start = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    table = torch.from_numpy(c.table).cuda()
+    for i in range(steps):
+        kv_len += 1
+        kw = dict(k_cache=kc, v_cache=vc, q_start=q_start, kv_len=kv_len, block_table=table, ws=ws)
+        v.kv_append(desc, k=dev[1][i], v=dev[2][i], **kw)
+        v.paged_attention(desc, q=dev[0][i], out=outs[i, 0], **kw)
+        v.block_sparse_attention(desc, q=dev[0][i], out=outs[i, 1], idx=idx, n_local=1, **kw)
+    assert v.device_status(ws) == 0
+    got, u = outs.double().cpu(), 2.0 ** -11
+    for b in range(2):
+        k = torch.cat((first[0][:100 * (b == 0)], ks[:, b])).double()
+        x = torch.cat((first[1][:100 * (b == 0)], xs[:, b])).double()
+        for i in range(steps):
+            m = (100 if b == 0 else 0) + i + 1
+            for h in range(8):
+                s = k[:m, h // 4] @ qs[i, b, h].double() / 8.0
+                w = s.softmax(0)
+                want = w @ x[:m, h // 4]
+                tol = u * want.abs() + (u + 2.0 ** -14) * (w @ x[:m, h // 4].abs()) * (1 + u)
+                # every block is the first or the last: both calls see all keys
+                for j in range(2):
+                    assert ((got[i, j, b, h] - want).abs() <= tol).all(), (i, j, b, h)
