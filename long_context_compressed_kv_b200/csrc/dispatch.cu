@@ -45,7 +45,7 @@ cudaError_t project_dispatch(const ProjectParams& P, cudaStream_t st) {
 }
 
 const char* build_info_string() {
-  return "v4attn sm_100a: compress(simt) index(mxfp4: tcgen05 mxf4; f32: simt) topk(cluster radix | radix) mqa(e4m3: tcgen05 fp8/bf16; f32: simt) project(bf16: tcgen05 f16; f32: simt)";
+  return "v4attn sm_100a: compress(simt) index(mxfp4: tcgen05 mxf4; f32: simt) topk(cluster radix | radix) mqa(e4m3: tcgen05 fp8/bf16; f32: simt) project(bf16: tcgen05 f16; f32: simt) kv(append: simt; attention: tcgen05 f16)";
 }
 
 }  // namespace v4a

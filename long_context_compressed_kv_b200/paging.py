@@ -14,7 +14,10 @@ on the host:
   as the sequence extends, released when it ends; ``tensor()`` gives the int32
   [B][blocks_per_seq] table the calls take (-1 marks a block not allocated);
 * ``pool_rows`` / ``scatter_to_pool`` - the pool row of an entry, and a
-  per-sequence cache copied into a pool (for moving existing caches over).
+  per-sequence cache copied into a pool (for moving existing caches over);
+* ``kv_pools`` - the K and V pools of an uncompressed layer, whose blocks hold
+  the same 128 tokens (``kv_append``, ``paged_attention``,
+  ``block_sparse_attention``).
 
 One table can serve every layer of a sequence: each layer keeps its own pools,
 all indexed by the same block ids (32 rows a block in a CSA layer's entry and
@@ -136,3 +139,11 @@ def scatter_to_pool(rows: torch.Tensor, table: np.ndarray, m: int,
         dst = torch.from_numpy(table[b, ids].astype(np.int64)).to(rows.device)
         view[dst] = src[idx]
     return pool
+
+
+def kv_pools(desc, n_blocks: int, device="cuda"):
+    """Zeroed K and V pools [n_blocks][Hkv][128][d] of a 16-bit K/V layer
+    (``kv_desc``), for the block ids 0 .. n_blocks-1 of a ``BlockPool``."""
+    from . import _KV_TORCH
+    shape = (n_blocks, desc.Hkv, BLOCK_TOKENS, desc.d)
+    return tuple(torch.zeros(shape, dtype=_KV_TORCH[desc.dtype], device=device) for _ in range(2))

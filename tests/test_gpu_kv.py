@@ -364,15 +364,14 @@ def _generate(c_seed, Hq, Hkv, d, dtype, chunks, sparse):
     """Chunks of new tokens of two sequences through append and attention on
     paging's block tables; returns every chunk's outputs and the whole history."""
     v = v4()
-    from long_context_compressed_kv_b200.paging import BlockPool, BlockTable
+    from long_context_compressed_kv_b200.paging import BlockPool, BlockTable, kv_pools
     dt = ku.DT[dtype]
     g = torch.Generator().manual_seed(c_seed)
     pool = BlockPool(24)
     table = BlockTable(2, 10, pool)
     desc = v.kv_desc(Hq, Hkv, d, dtype=dt, rope_halves=True)
     ws = v.kv_workspace(desc)
-    kc = torch.full((24, Hkv, BLOCK, d), math.nan, dtype=dt, device="cuda")
-    vc = kc.clone()
+    kc, vc = (x.fill_(math.nan) for x in kv_pools(desc, 24))
     lens = [0, 0]
     hist, res = [[], []], []
     for n in chunks:

@@ -132,3 +132,11 @@ def test_the_binding_refuses_wrong_tensors():
         # the last: tensors that are not on a GPU
         with pytest.raises(ValueError):
             v.kv_append(d, **{**good, **bad})
+
+
+def test_pools_of_a_layer():
+    import long_context_compressed_kv_b200 as v
+    from long_context_compressed_kv_b200.paging import kv_pools
+    k, x = kv_pools(v.kv_desc(8, 2, 64, dtype=torch.float16), 5, device="cpu")
+    assert k.shape == x.shape == (5, 2, 128, 64) and k.dtype == torch.float16
+    assert k.data_ptr() != x.data_ptr() and not k.any()
