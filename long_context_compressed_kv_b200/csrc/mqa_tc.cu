@@ -737,6 +737,11 @@ __global__ void __launch_bounds__(NTHR, 1)
         uint32_t r[32];
         tmem_ld32_nowait(ob + c, r);
         tmem_ld_wait();
+        // a split without keys has written no O: what the TMEM holds may be
+        // anything of an earlier kernel, NaN too (which 0 would not clear)
+        if (!(lr > 0.f))
+#pragma unroll
+          for (int k = 0; k < 32; ++k) r[k] = 0;
         uint32_t hv[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -897,6 +902,9 @@ __global__ void __launch_bounds__(NTHR, 1)
         uint32_t r[32];
         tmem_ld32_nowait(ob + c, r);
         tmem_ld_wait();
+        if (f == 0.f)                                        // as above
+#pragma unroll
+          for (int k = 0; k < 32; ++k) r[k] = 0;
         if (row_h(hh) < P.H)
 #pragma unroll
           for (int k = 0; k < 32; k += 4)

@@ -763,3 +763,37 @@ def test_calls_in_a_row_on_one_stream():
                 # every block is the first or the last: both calls see all keys
                 for j in range(2):
                     assert ((got[i, j, b, h] - want).abs() <= tol).all(), (i, j, b, h)
+
+
+def test_compressed_layers_after_nan_in_tensor_memory():
+    """Tensor memory keeps what a kernel leaves there, NaN here; a dense MQA
+    whose queries see few entries (splits without a key, and in the form
+    without splits queries of an empty history) does not take it up."""
+    import synth
+    from tests.gpu_util import code_rows, desc_for, dev
+    v = v4()
+    rng = np.random.default_rng(3)
+    m, H, d, N, B = 128, 128, 512, 700, 3
+    ldesc = desc_for(synth.Layer("hca", m, H, d, 64, 128, 4, 32, 96))
+    kv, kv_sc = code_rows(ldesc, dev(rng.standard_normal((B, N, d)).astype(np.float32)),
+                          v.E4M3_BF16ROPE, d_rope=64)
+    swa, swa_sc = code_rows(ldesc, dev(rng.standard_normal((B, 256, d)).astype(np.float32)),
+                            v.E4M3_BF16ROPE, d_rope=64)
+    for nq in (6, 90):
+        pos = rng.integers(0, 600, nq)
+        pos[:3] = m * N - 1, 5, -1
+        seq = rng.integers(0, B, nq)
+        out = torch.zeros(nq, H, d, device="cuda")
+        ws = v.workspace(ldesc, nq, N)
+        q = dev(rng.standard_normal((nq, H, d)).astype(np.float32), torch.bfloat16)
+        c = Case([1] * 40, [5000] + [130] * 39, 8, 8, 128, seed=1)
+        c.k_pool.fill_(math.nan)
+        c.v_pool.fill_(math.nan)
+        nan_out, _ = attend(c)
+        assert nan_out.isnan().all()
+        v.dense_mqa(ldesc, Q=q, q_pos=dev(pos, torch.int64), q_seq=dev(seq, torch.int32), B=B,
+                    kv=kv, kv_scale=kv_sc, kv_rows=N, swa=swa, swa_scale=swa_sc, swa_rows=256,
+                    max_vis=N, out=out, ws=ws)
+        assert v.device_status(ws) == 0
+        assert out.isfinite().all()
+        assert (out[2] == 0).all()
