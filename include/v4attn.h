@@ -380,8 +380,10 @@ typedef struct {
  *   s_j = softmax_scale q . k_j,  den = exp(sink_h) + sum_j exp(s_j)
  *   out = sum_j exp(s_j) v_j / den,  lse = log den
  * A query that sees no key gets out = 0 and lse = sink_h (-inf without sinks).
- * q . k, the softmax and its sums are fp32, exp(s_j) enters the product with
- * v_j in the cache's type.  Rows past a sequence's kv_len, rows of blocks that
+ * q . k, the softmax and its sums are fp32; exp(s_j), less a row's common
+ * factor, enters the product with v_j rounded to the cache's type.  How the keys
+ * are cut over CTAs, and with it the order of the fp32 sums, depends on the
+ * whole batch; the same call gives the same bits.  Rows past a sequence's kv_len, rows of blocks that
  * no query of a call sees and rows before the first window may hold anything;
  * a non-finite value in a row that some query of the call sees may reach the
  * other queries of its sequence. */
