@@ -301,7 +301,7 @@ def _kv_cache(d, Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table, ws)
     if kv_len.dim() != 1 or block_table.dim() != 2 or k_cache.dim() != 4:
         raise ValueError("kv_len is [B], block_table [B][blocks_per_seq], a cache "
                          "[n_blocks][Hkv][128][d]")
-    n, B, bps = len(k_cache), len(kv_len), block_table.shape[1]
+    n, B, bps = k_cache.shape[0], kv_len.shape[0], block_table.shape[1]
     pool = (n, Hkv, 128, d)
     return dev, B, (_kv_small("k_cache", k_cache, pool, dtype, dev),
                     _kv_small("v_cache", v_cache, pool, dtype, dev), n,
@@ -315,9 +315,9 @@ _KV_CALLS = {fn: (_abi.packed_call(fn), fmt.pack) for fn, fmt in _abi.PACKED.ite
 
 def _kv_call(fn, desc, dev, ws, stream, *values):
     call, pack = _KV_CALLS[fn]
-    args, ws_p, ws_n = pack(*values), ws.data_ptr(), ws.numel() * ws.element_size()
+    args, ws_p, ws_n = pack(*values), ws.data_ptr(), ws.nbytes
     at = ctypes.addressof(desc)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = call(at, args, ws_p, ws_n, _raw_stream(dev, stream))
     else:       # on the tensors' device, whichever is current
         with torch.cuda.device(dev):
@@ -340,7 +340,7 @@ def kv_append(desc: KvDesc, *, k, v, k_cache, v_cache, q_start, kv_len, block_ta
     included), block_table int32 [B][blocks_per_seq]."""
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    d, Hkv, dtype, T = desc.d, desc.Hkv, _KV_TORCH.get(desc.dtype), len(k)
+    d, Hkv, dtype, T = desc.d, desc.Hkv, _KV_TORCH.get(desc.dtype), k.shape[0]
     dev, B, cache = _kv_cache(d, Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table, ws)
     kv = (T, Hkv, d)
     if q is None:
@@ -354,7 +354,7 @@ def kv_append(desc: KvDesc, *, k, v, k_cache, v_cache, q_start, kv_len, block_ta
 
 def _kv_attention(fn, desc, q, k_cache, v_cache, q_start, kv_len, block_table, out, ws, lse, sink,
                   idx, n_local, stream):
-    d, Hq, dtype, T = desc.d, desc.Hq, _KV_TORCH.get(desc.dtype), len(q)
+    d, Hq, dtype, T = desc.d, desc.Hq, _KV_TORCH.get(desc.dtype), q.shape[0]
     dev, B, cache = _kv_cache(d, desc.Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table,
                               ws)
     rows = (T, Hq, d)
