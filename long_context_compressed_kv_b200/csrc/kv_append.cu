@@ -63,6 +63,9 @@ template <bool F16, int NT, int NB>
 __global__ void __launch_bounds__(NT) kv_append_kernel(const __grid_constant__ KvAppendParams P) {
   __shared__ float2 cs[64];
   const int t = blockIdx.x, tid = threadIdx.x;
+  // launched while the grid before still runs (as the attention behind it is)
+  next_grid();
+  wait_grid();
   const int lu = P.d == 128 ? 3 : 2, units = 1 << lu;      // units of 16 values in a row
   const int keep = (P.d - P.d_rope) / 16, half = P.d_rope / 2;
   const int hq = P.q.p ? P.Hq : 0;
@@ -161,11 +164,18 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(const __grid_constant__ K
 
 namespace {
 template <int NT, int NB>
-void launch(const KvAppendParams& P, cudaStream_t st) {
-  if (P.f16)
-    kv_append_kernel<true, NT, NB><<<P.b.T, NT, 0, st>>>(P);
-  else
-    kv_append_kernel<false, NT, NB><<<P.b.T, NT, 0, st>>>(P);
+cudaError_t launch(const KvAppendParams& P, cudaStream_t st) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(P.b.T, 1, 1);
+  cfg.blockDim = dim3(NT, 1, 1);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return P.f16 ? cudaLaunchKernelEx(&cfg, kv_append_kernel<true, NT, NB>, P)
+               : cudaLaunchKernelEx(&cfg, kv_append_kernel<false, NT, NB>, P);
 }
 }  // namespace
 
@@ -174,11 +184,7 @@ cudaError_t launch_kv_append(const KvAppendParams& P, cudaStream_t st) {
   // for 8192 tokens and 3.2 us for 16 on 320 threads, 55.6 and 4.5 us on 128; 40
   // rows of 64 (160 units) 5.8 us for 1204 tokens on 320, 3.9 us on 128.
   const int units = ((P.q.p ? P.Hq : 0) + 2 * P.Hkv) * P.d / 16;
-  if (units > 256)
-    launch<320, 2>(P, st);
-  else
-    launch<128, 3>(P, st);
-  return cudaGetLastError();
+  return units > 256 ? launch<320, 2>(P, st) : launch<128, 3>(P, st);
 }
 
 }  // namespace v4a

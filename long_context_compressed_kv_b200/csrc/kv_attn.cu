@@ -38,6 +38,8 @@
 // Warps: 0-3 / 4-7 softmax of slot 0 / 1 (a thread a row, TMEM lane quarter =
 // warp % 4), 8 MMA issue, 9 work list and TMA loads, 10-11 idle (they complete the
 // third warpgroup, whose registers the softmax warpgroups take over).
+#include <algorithm>
+
 #include "common.cuh"
 #include "kv_kernels.h"
 #include "tc_common.cuh"
@@ -188,14 +190,6 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// The kernels of a call, and calls in a row, are launched while the one before
-// still runs (programmatic dependent launch): no global memory is touched before
-// wait_grid(), which returns when the grid before is complete and flushed.
-__device__ __forceinline__ void wait_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void next_grid() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -1259,7 +1253,8 @@ cudaError_t launch(const KvAttnParams& P, const CUtensorMap& q, const CUtensorMa
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, F16, SPARSE>, P, q, k, v);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(grid, 16, 1);
+  // rows of an item: at most two tiles, at most the call's tokens
+  cfg.gridDim = dim3(grid, std::min(16, std::min(P.b.T, 2 * P.tt) * P.g), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, F16>, P, grid);

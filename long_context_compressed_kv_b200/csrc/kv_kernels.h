@@ -12,6 +12,16 @@ constexpr int kKvMaxSel = 2048;     // entries of a query's block list
 constexpr int kKvMaxCtas = 160;     // CTAs of the attention kernel (one an SM)
 constexpr int kKvPartRows = 256;    // rows of an item: two tiles
 
+#if defined(__CUDACC__)
+// The kernels of a call, and calls in a row, are launched while the one before
+// still runs (programmatic dependent launch): no global memory is touched before
+// wait_grid(), which returns when the grid before is complete and flushed.
+__device__ __forceinline__ void wait_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_grid() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+#endif
+
 // A ragged batch of new tokens over paged caches (see "16-bit K/V layers" in
 // v4attn.h).
 struct KvBatch {
