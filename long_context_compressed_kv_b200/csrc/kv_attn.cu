@@ -197,6 +197,7 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
 }
+
 // ---------------------------------------------------------------- work list
 // Everything below is a function of the lengths alone, so every CTA finds its
 // own range without a word from the others.
@@ -693,8 +694,8 @@ struct Kernel {
       open[slot] = true;
       return true;
     };
-    // the P V still to issue of a slot (pend: its V tile), once P is there; V:
-    // whether the tile is known to have landed
+    // the P V still to issue of a slot (pend: its V tile), once P is there
+    // (landed: the tile is known to be)
     auto flush = [&](int slot, bool landed) -> bool {
       if (pend[slot] < 0) return true;
       if (!landed && !wait_tile(pend[slot])) return false;
@@ -824,7 +825,7 @@ struct Kernel {
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = lanes + TM_S + slot * NK, t_o = lanes + TM_O + slot * D;
     const float sl2 = P.scale * kLog2e;
-    const float grow = kGrow / sl2;
+    const float grow = fminf(kGrow / sl2, 1e37f);            // finite: a row's first key passes -inf
     const int rt = r / P.g, rh = r - rt * P.g;               // token and head of this row
     int ns = 0, no1 = 0;
     wait_grid();

@@ -102,10 +102,12 @@ def test_long_histories_and_few_rows():
     assert all(torch.equal(x, y) for x, y in zip(first, again))
 
 
-def test_softmax_scale_and_large_logits():
-    c = Case([3, 40], [500, 300], 8, 2, 64, seed=8, q_scale=12.0)
-    out, lse = attend(c, scale=0.9)
-    check(c, out, lse, reference(c, scale=float(np.float32(0.9))))
+@pytest.mark.parametrize("scale,q_scale", [(0.9, 12.0), (1e-39, 1.0), (1e-6, 1.0)])
+def test_softmax_scale_and_large_logits(scale, q_scale):
+    """Large logits, and scales so small (one a denormal) that every key weighs the same."""
+    c = Case([3, 40], [500, 300], 8, 2, 64, seed=8, q_scale=q_scale)
+    out, lse = attend(c, scale=scale)
+    check(c, out, lse, reference(c, scale=float(np.float32(scale))))
 
 
 def test_growing_maximum():
