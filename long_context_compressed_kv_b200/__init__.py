@@ -293,41 +293,50 @@ def _kv_small(name, t, shape, dtype, dev):
     return t.data_ptr()
 
 
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+
+
 def _kv_cache(d, Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table, ws):
     """Checked (device, B, pool and table fields) of a call on a 16-bit K/V layer."""
     dev = k_cache.get_device()
-    if dev < 0 or ws.get_device() != dev:
-        raise ValueError(f"tensors must live on one GPU, got {k_cache.device} and {ws.device}")
-    if kv_len.dim() != 1 or block_table.dim() != 2 or k_cache.dim() != 4:
-        raise ValueError("kv_len is [B], block_table [B][blocks_per_seq], a cache "
-                         "[n_blocks][Hkv][128][d]")
-    n, B, bps = k_cache.shape[0], kv_len.shape[0], block_table.shape[1]
-    pool = (n, Hkv, 128, d)
-    return dev, B, (_kv_small("k_cache", k_cache, pool, dtype, dev),
-                    _kv_small("v_cache", v_cache, pool, dtype, dev), n,
-                    _kv_small("q_start", q_start, (B + 1,), torch.int32, dev),
-                    _kv_small("kv_len", kv_len, (B,), torch.int64, dev),
-                    _kv_small("block_table", block_table, (B, bps), torch.int32, dev), bps)
+    pool, table = k_cache.shape, block_table.shape
+    if len(pool) != 4 or len(table) != 2:
+        raise ValueError("a cache is [n_blocks][Hkv][128][d], block_table [B][blocks_per_seq]")
+    (n, H, rows, dims), (B, bps) = pool, table
+    if (dev < 0 or v_cache.get_device() != dev or q_start.get_device() != dev
+            or kv_len.get_device() != dev or block_table.get_device() != dev
+            or ws.get_device() != dev):
+        raise ValueError("k_cache, v_cache, q_start, kv_len, block_table and ws must live on one GPU")
+    if (H != Hkv or rows != 128 or dims != d or v_cache.shape != pool or k_cache.dtype is not dtype
+            or v_cache.dtype is not dtype or not k_cache.is_contiguous()
+            or not v_cache.is_contiguous()):
+        raise ValueError(f"k_cache and v_cache must be contiguous [n_blocks][{Hkv}][128][{d}] in "
+                         f"{dtype}, got {tuple(pool)} in {k_cache.dtype}, {tuple(v_cache.shape)} in "
+                         f"{v_cache.dtype}")
+    if (q_start.dtype is not _I32 or kv_len.dtype is not _I64 or block_table.dtype is not _I32
+            or q_start.shape != (B + 1,) or kv_len.shape != (B,) or not q_start.is_contiguous()
+            or not kv_len.is_contiguous() or not block_table.is_contiguous()):
+        raise ValueError("q_start int32 [B + 1], kv_len int64 [B] and block_table int32 "
+                         f"[B][blocks_per_seq] must be contiguous, got {tuple(q_start.shape)} in "
+                         f"{q_start.dtype}, {tuple(kv_len.shape)} in {kv_len.dtype}, "
+                         f"{tuple(table)} in {block_table.dtype}")
+    return dev, B, (k_cache.data_ptr(), v_cache.data_ptr(), n, q_start.data_ptr(),
+                    kv_len.data_ptr(), block_table.data_ptr(), bps)
 
 
 _KV_CALLS = {fn: (_abi.packed_call(fn), fmt.pack) for fn, fmt in _abi.PACKED.items()}
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _kv_call(fn, desc, dev, ws, stream, *values):
     call, pack = _KV_CALLS[fn]
-    args, ws_p, ws_n = pack(*values), ws.data_ptr(), ws.nbytes
-    at = ctypes.addressof(desc)
-    if torch._C._cuda_getDevice() == dev:
-        status = call(at, args, ws_p, ws_n, _raw_stream(dev, stream))
-    else:       # on the tensors' device, whichever is current
+    if _current_device() != dev:       # on the tensors' device, whichever is current
         with torch.cuda.device(dev):
-            status = call(at, args, ws_p, ws_n, _raw_stream(dev, stream))
-    if status != _abi.OK:
+            return _kv_call(fn, desc, dev, ws, stream, *values)
+    status = call(ctypes.addressof(desc), pack(*values), ws.data_ptr(), ws.nbytes,
+                  _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
         raise V4AttnError(fn, status)
-
-
-def _raw_stream(dev: int, stream) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def kv_append(desc: KvDesc, *, k, v, k_cache, v_cache, q_start, kv_len, block_table, ws, q=None,
@@ -363,12 +372,12 @@ def _kv_attention(fn, desc, q, k_cache, v_cache, q_start, kv_len, block_table, o
         if idx.dim() not in (2, 3):
             raise ValueError("idx must be [T][n_lists][n_sel] or [T][n_sel]")
         n_lists, n_sel = idx.shape[1] if idx.dim() == 3 else 1, idx.shape[-1]
-        idx = _kv_small("idx", idx, (T, *idx.shape[1:]), torch.int32, dev)
+        idx = _kv_small("idx", idx, (T, *idx.shape[1:]), _I32, dev)
     _kv_call(fn, desc, dev, ws, stream, T, B, *_kv_rows("q", q, rows, dtype, dev), *cache,
              idx or 0, n_lists, n_sel, n_local,
-             0 if sink is None else _kv_small("sink", sink, (Hq,), torch.float32, dev),
+             0 if sink is None else _kv_small("sink", sink, (Hq,), _F32, dev),
              *_kv_rows("out", out, rows, dtype, dev),
-             0 if lse is None else _kv_small("lse", lse, (T, Hq), torch.float32, dev))
+             0 if lse is None else _kv_small("lse", lse, (T, Hq), _F32, dev))
 
 
 def paged_attention(desc: KvDesc, *, q, k_cache, v_cache, q_start, kv_len, block_table, out, ws,
