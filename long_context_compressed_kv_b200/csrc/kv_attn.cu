@@ -25,7 +25,10 @@
 //   more than tt tokens (chunks): a slot a tile, both on the same key blocks,
 //     so a block is loaded once for 256 rows;
 //   else (decode steps): both slots hold the one tile, even and odd blocks,
-//     merged at the end.
+//     merged at the end.  Up to 64 rows are MMAs of M = 64, row r in lane
+//     32 (r / 16) + r % 16: the same time, but less power, and so a higher clock
+//     under the power cap (32 steps of up to 16384 positions, after some seconds:
+//     194 us at 1.58 GHz with M = 128, 183 at 1.71).
 // The MMA thread issues P V of one slot and the next Q K^T of the same slot
 // while the other slot's warps work on their scores.
 //
@@ -76,6 +79,7 @@ constexpr int kMinRange = 1;
 struct Piece {
   int n;             // blocks
   int dual;          // two tiles (a slot each) or one
+  int half;          // one, of at most 64 rows
   int first, last;   // of the item's blocks in this CTA's range
   int part;          // -1: the whole item, rows go to the output; else the part to write
   int b, h, tok0, ntok;   // sequence, K/V head, first token row, tokens
@@ -459,6 +463,7 @@ struct Kernel {
             const int e0 = max(c0 - kItemCost, 0), e1 = max(c1 - kItemCost, 0);
             Piece pc;
             pc.dual = i1 - i0 > tt;
+            pc.half = (i1 - i0) * P.g <= MROWS / 2;
             pc.b = w.b0 + src;
             pc.h = h;
             pc.tok0 = q.q0 + i0;
@@ -648,13 +653,19 @@ struct Kernel {
     constexpr uint64_t k_bits = smem_desc_bits(16, 1024, 2);             // K-major, 128B swizzle
     constexpr uint64_t v_bits = smem_desc_bits(MROWS * 128, 1024, 2);    // MN-major, 128B swizzle
     constexpr uint32_t fmt = F16 ? 0 : 1;
-    constexpr uint32_t id_qk = idesc_f(fmt, fmt, MROWS, NK, false, false);
-    constexpr uint32_t id_pv = idesc_f(fmt, fmt, MROWS, D, false, true);
+    auto id_qk = [](int half) {
+      return half ? idesc_f(fmt, fmt, MROWS / 2, NK, false, false)
+                  : idesc_f(fmt, fmt, MROWS, NK, false, false);
+    };
+    auto id_pv = [](int half) {
+      return half ? idesc_f(fmt, fmt, MROWS / 2, D, false, true)
+                  : idesc_f(fmt, fmt, MROWS, D, false, true);
+    };
     const uint32_t q_at = smem_u32(s.q) >> 4, kv_at = smem_u32(s.kv) >> 4;
     int base = 0, items = 0, np[2] = {0, 0}, ne[2] = {0, 0}, pend[2] = {-1, -1};
     uint32_t acc[2] = {0, 0};
     auto wait_tile = [&](int i) { return mbar_wait_at(&s.full[i % NST], (i / NST) & 1, status, 3); };
-    auto qk = [&](int slot, int qslot, int tile) {
+    auto qk = [&](int slot, int qslot, int tile, int half) {
       tc_fence_after();
       const uint64_t a = k_bits | (q_at + qslot * (C::kTile / 16));
       const uint64_t b = k_bits | (kv_at + tile % NST * (C::kTile / 16));
@@ -662,16 +673,16 @@ struct Kernel {
       for (int kk = 0; kk < D / 16; ++kk) {
         // 64 dims (4 steps of 32 bytes) a swizzled half of 128 rows x 128 bytes
         const uint32_t off = (kk / 4) * (MROWS * 128 / 16) + (kk % 4) * 2;
-        mma_f16(TM_S + slot * NK, a + off, b + off, id_qk, kk > 0);
+        mma_f16(TM_S + slot * NK, a + off, b + off, id_qk(half), kk > 0);
       }
     };
-    auto pv = [&](int slot, int tile, bool rest) {
+    auto pv = [&](int slot, int tile, bool rest, int half) {
       tc_fence_after();
       const uint64_t b = v_bits | (kv_at + tile % NST * (C::kTile / 16));
 #pragma unroll
       for (int kk = 0; kk < NK / 16; ++kk)        // 16 keys: 8 columns of P, 16 rows x 128 bytes
         if ((kk >= kEarly / 16) == rest)
-          mma_f16_ts(TM_O + slot * D, TM_S + slot * NK + 8 * kk, b + 128 * kk, id_pv,
+          mma_f16_ts(TM_O + slot * D, TM_S + slot * NK + 8 * kk, b + 128 * kk, id_pv(half),
                  kk > 0 ? 1u : acc[slot]);
       if (rest) acc[slot] = 1;
     };
@@ -696,14 +707,14 @@ struct Kernel {
     };
     // the P V still to issue of a slot (pend: its V tile), once P is there
     // (landed: the tile is known to be)
-    auto flush = [&](int slot, bool landed) -> bool {
+    auto flush = [&](int slot, bool landed, int half) -> bool {
       if (pend[slot] < 0) return true;
       if (!landed && !wait_tile(pend[slot])) return false;
       if (!mbar_wait_at(&s.pearly[slot], ne[slot] & 1, status, 14)) return false;
       ++ne[slot];
-      pv(slot, pend[slot], false);
+      pv(slot, pend[slot], false, half);
       if (!answered(slot)) return false;
-      pv(slot, pend[slot], true);
+      pv(slot, pend[slot], true, half);
       pend[slot] = -1;
       return true;
     };
@@ -713,7 +724,7 @@ struct Kernel {
       if (!mbar_wait_at(&s.pfull[pi], (pieces >> 1) & 1, status, 4)) break;
       const int n = s.piece[pi].n, dual = s.piece[pi].dual,
                 first = s.piece[pi].first, last = s.piece[pi].last,
-                end = s.piece[pi].end;
+                end = s.piece[pi].end, half = s.piece[pi].half;
       mbar_arrive(&s.pempty[pi]);
       if (end) break;
       if (first) {
@@ -734,7 +745,7 @@ struct Kernel {
           const bool both = !SPARSE || (pend[0] >= 0 && pend[1] >= 0);
 #pragma unroll
           for (int slot = 0; slot < 2; ++slot) {
-            if (!(ok = ok && flush(slot, slot == 1 && both))) break;
+            if (!(ok = ok && flush(slot, slot == 1 && both, 0))) break;
             if (slot == 1 && i > 0) tc_commit(&s.empty[(kt - 1) % NST]);
             if (i == n) {
               ok = signal(slot, -1, 0, 0);
@@ -746,7 +757,7 @@ struct Kernel {
               mask = SPARSE ? s.mask[mi] : 0xffffffffu;
             }
             if (!SPARSE || ((mask >> (slot * P.tt)) & tile_bits)) {
-              qk(slot, slot, kt);
+              qk(slot, slot, kt, 0);
               ok = signal(slot, kt + 1, blk, mask);
               pend[slot] = kt + 1;
             }
@@ -760,14 +771,14 @@ struct Kernel {
             const int j = i + slot, kt = base + 2 * j, mi = (kt >> 1) % kMeta;
             if (!ok || j >= n + 2) break;
             const bool had = pend[slot] >= 0;
-            if (!(ok = flush(slot, false))) break;
+            if (!(ok = flush(slot, false, half))) break;
             if (had) tc_commit(&s.empty[(kt - 3) % NST]);
             if (j >= n) {
               ok = signal(slot, -1, 0, 0);
               continue;
             }
             if (!(ok = wait_tile(kt))) break;
-            qk(slot, 0, kt);
+            qk(slot, 0, kt, half);
             tc_commit(&s.empty[kt % NST]);
             ok = signal(slot, kt + 1, s.blk[mi], SPARSE ? s.mask[mi] : 0xffffffffu);
             pend[slot] = kt + 1;
@@ -826,7 +837,6 @@ struct Kernel {
     const uint32_t t_s = lanes + TM_S + slot * NK, t_o = lanes + TM_O + slot * D;
     const float sl2 = P.scale * kLog2e;
     const float grow = fminf(kGrow / sl2, 1e37f);            // finite: a row's first key passes -inf
-    const int rt = r / P.g, rh = r - rt * P.g;               // token and head of this row
     int ns = 0, no1 = 0;
     wait_grid();
     float m = -INFINITY, l = 0.f;
@@ -841,6 +851,9 @@ struct Kernel {
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.pempty[pi]);
       };
+      // this lane's row of the tile (MROWS: none), its token and head
+      const int row = !pc.half ? r : lane < 16 ? (warp & 3) * 16 + lane : MROWS;
+      const int rt = row / P.g, rh = row - rt * P.g;
       const int tok = rt + (pc.dual ? slot * P.tt : 0);      // of the item
       const bool valid = rt < P.tt && tok < pc.ntok;
       const bool active = __any_sync(0xffffffffu, valid);
@@ -992,7 +1005,7 @@ struct Kernel {
           P.lse[(int64_t)(pc.tok0 + tok) * P.Hq + hq] = log_sum(top, l, m == -INFINITY, P.sink, hq);
         f = l == 0.f ? 0.f : f / l;
       } else if (valid) {
-        float2* ml = P.part_ml + (int64_t)part * (2 * MROWS) + (pc.dual ? slot * MROWS : 0) + r;
+        float2* ml = P.part_ml + (int64_t)part * (2 * MROWS) + (pc.dual ? slot * MROWS : 0) + row;
         *ml = make_float2(top, l);
       }
       __syncwarp();
@@ -1001,7 +1014,7 @@ struct Kernel {
                         (int64_t)(pc.tok0 + tok) * P.out.tok +
                         (int64_t)(pc.h * P.g + rh) * P.out.head;
         float* part_o = P.part_o +
-                        ((int64_t)part * (2 * MROWS) + (pc.dual ? slot * MROWS : 0) + r) * D;
+                        ((int64_t)part * (2 * MROWS) + (pc.dual ? slot * MROWS : 0) + row) * D;
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           uint32_t o[16], o1[16];
