@@ -12,10 +12,10 @@
 // half a step at most, as the output is by its own rounding.
 //
 // Bounds.  Decode steps: HBM, 8 (g = 8) FLOP a byte.  32 steps of up to 16384
-// positions, 64 heads on 8, d = 128: 173 us, 6.4 TB/s of K and V.  Chunks: the
+// positions, 64 heads on 8, d = 128: 172 us, 6.4 TB/s of K and V.  Chunks: the
 // tensor pipe (2 x 1024 of its cycles a block and pair of tiles), short of that
 // the chain scores -> P -> P V -> next scores of a slot, which the other slot's
-// half hides: 2048 tokens on 32768: 1.76 ms, 1.2 PFLOP/s, pipe 59% busy.  Short
+// half hides: 2048 tokens on 32768: 1.75 ms, 1.2 PFLOP/s, pipe 59% busy.  Short
 // calls: launch, work list, first load and merge, about 10 us.
 //
 // Rows.  The g = Hq / Hkv query heads that share a K/V head are rows of one
@@ -23,12 +23,15 @@
 // is (sequence, K/V head, up to 2 tt tokens).  A CTA has two slots, each with
 // its own S / P and O in TMEM and its own softmax warpgroup:
 //   more than tt tokens (chunks): a slot a tile, both on the same key blocks,
-//     so a block is loaded once for 256 rows;
+//     so a block is loaded once for 256 rows; a block that no row of a tile sees
+//     (past the diagonal, before the window, not selected) its slot skips (four
+//     prompts of up to 4096, 32 heads, after some seconds: 460 us without, 443
+//     with; 2048 tokens on 32768: 2079 and 2067);
 //   else (decode steps): both slots hold the one tile, even and odd blocks,
 //     merged at the end.  Up to 64 rows are MMAs of M = 64, row r in lane
 //     32 (r / 16) + r % 16: the same time, but less power, and so a higher clock
 //     under the power cap (32 steps of up to 16384 positions, after some seconds:
-//     194 us at 1.58 GHz with M = 128, 183 at 1.71).
+//     194 us at 1.58 GHz with M = 128, 181 at 1.71).
 // The MMA thread issues P V of one slot and the next Q K^T of the same slot
 // while the other slot's warps work on their scores.
 //
@@ -80,6 +83,7 @@ struct Piece {
   int n;             // blocks
   int dual;          // two tiles (a slot each) or one
   int half;          // one, of at most 64 rows
+  int to0, from1;    // dense, two tiles: slot 0 takes blocks 0 .. to0-1, slot 1 from1 .. n-1
   int first, last;   // of the item's blocks in this CTA's range
   int part;          // -1: the whole item, rows go to the output; else the part to write
   int b, h, tok0, ntok;   // sequence, K/V head, first token row, tokens
@@ -489,6 +493,10 @@ struct Kernel {
             if (!SPARSE) {
               pc.first = pc.last = 1;
               pc.n = e1 - e0;
+              // of two tiles the first may end before the last block, and the
+              // windows of the second may begin behind the first
+              pc.to0 = min(pc.n, (pc.pos0 + tt - 1) / NK - sp.lo - e0 + 1);
+              pc.from1 = P.n_win ? max(0, (pc.pos0 + tt - P.n_win + 1) / NK - sp.lo - e0) : 0;
               ok = ok && publish(pc);
               for (int e = e0; ok && e < e1; e += 32) {
                 if (e > e0) pb = entry(pc.b, sp.lo + e + lane, e + lane < e1);
@@ -724,7 +732,8 @@ struct Kernel {
       if (!mbar_wait_at(&s.pfull[pi], (pieces >> 1) & 1, status, 4)) break;
       const int n = s.piece[pi].n, dual = s.piece[pi].dual,
                 first = s.piece[pi].first, last = s.piece[pi].last,
-                end = s.piece[pi].end, half = s.piece[pi].half;
+                end = s.piece[pi].end, half = s.piece[pi].half, to0 = s.piece[pi].to0,
+                from1 = s.piece[pi].from1;
       mbar_arrive(&s.pempty[pi]);
       if (end) break;
       if (first) {
@@ -742,7 +751,7 @@ struct Kernel {
           const int kt = base + 2 * i, mi = (kt >> 1) % kMeta;
           int blk = 0;
           uint32_t mask = 0;
-          const bool both = !SPARSE || (pend[0] >= 0 && pend[1] >= 0);
+          const bool both = pend[0] >= 0 && pend[1] >= 0;
 #pragma unroll
           for (int slot = 0; slot < 2; ++slot) {
             if (!(ok = ok && flush(slot, slot == 1 && both, 0))) break;
@@ -756,7 +765,7 @@ struct Kernel {
               blk = s.blk[mi];
               mask = SPARSE ? s.mask[mi] : 0xffffffffu;
             }
-            if (!SPARSE || ((mask >> (slot * P.tt)) & tile_bits)) {
+            if (SPARSE ? ((mask >> (slot * P.tt)) & tile_bits) != 0 : slot ? i >= from1 : i < to0) {
               qk(slot, slot, kt, 0);
               ok = signal(slot, kt + 1, blk, mask);
               pend[slot] = kt + 1;

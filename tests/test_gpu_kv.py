@@ -613,6 +613,16 @@ def test_many_items_of_a_head():
     check(c, *select(c, idx, 1), reference(c, idx=idx, n_local=1))
 
 
+@pytest.mark.parametrize("n_win", [0, 1, 128, 1280])
+@pytest.mark.parametrize("ns,ls", [([16], [5128]), ([16], [1288]), ([16, 1, 40], [136, 4000, 3720])])
+def test_tiles_that_end_a_block_apart(ns, ls, n_win):
+    """Items of two tiles whose tokens lie on both sides of a block's end, as
+    parts of a block or two: one tile sees the last block, and with a window
+    the first, that the other does not, or nothing of its part."""
+    c = Case(ns, ls, 16, 1, 128, seed=ls[0] + n_win)
+    check(c, *attend(c, n_win), reference(c, n_win))
+
+
 def test_one_row_over_every_sm():
     """A single query head on a long history: as many parts as CTAs."""
     c = Case([1], [40000], 1, 1, 128, seed=5)
