@@ -613,6 +613,48 @@ def test_many_items_of_a_head():
     check(c, *select(c, idx, 1), reference(c, idx=idx, n_local=1))
 
 
+# at most 16 rows a sequence on average
+STEPS = [
+    ([1] * 5, [1, 129, 700, 128, 3000], 16, 1, 128, "bf16", 0),        # 16 rows each
+    ([4, 3, 0, 1, 4], [4, 300, 50, 1, 1000], 8, 2, 128, "fp16", 0),    # several tokens
+    ([16, 9, 16], [16, 140, 1000], 2, 2, 64, "bf16", 0),
+    ([5, 5, 1], [5, 1285, 128], 6, 2, 128, "bf16", 7),                 # 15 rows, windows
+    ([16, 16], [400, 261], 4, 4, 128, "fp16", 130),
+    ([1, 2], [2000, 1500], 16, 2, 64, "fp16", 300),
+    ([1] * 90 + [100] + [1] * 10, [200] * 90 + [333] + [150] * 10, 8, 1, 128, "bf16", 0),
+    ([2] * 60 + [20, 70, 130], [150] * 60 + [20, 300, 260], 4, 2, 64, "fp16", 0),
+    ([1] * 70 + [3, 20, 90], [130] * 70 + [700, 600, 900], 8, 1, 128, "bf16", 200),
+]
+
+
+@pytest.mark.parametrize("with_sink", [False, True])
+@pytest.mark.parametrize("ns,ls,Hq,Hkv,d,dtype,n_win", STEPS)
+def test_steps_of_few_rows(ns, ls, Hq, Hkv, d, dtype, n_win, with_sink):
+    """Decode steps, of one token and of several, alone and with longer
+    sequences among them; dense and over selected blocks."""
+    c = Case(ns, ls, Hq, Hkv, d, dtype, seed=len(ns) + Hq + n_win, front=2, behind=3)
+    sink = torch.randn(Hq, generator=torch.Generator().manual_seed(5)) if with_sink else None
+    check(c, *attend(c, n_win, sink), reference(c, n_win, sink))
+    idx = lists_for(c, Hkv, 3, seed=Hq, messy=with_sink)
+    check(c, *select(c, idx, 1, sink), reference(c, sink=sink, idx=idx, n_local=1))
+
+
+def test_maxima_that_grow_in_decode_steps():
+    """Logits that rise from block to block, at other rates for other heads and in
+    other warps' keys, so that maxima move in some rows of some blocks alone."""
+    for dtype, d in (("fp16", 128), ("bf16", 64)):
+        c = Case([1, 2], [2000, 1999], 16, 2, d, dtype, seed=3)
+        c.q = (torch.arange(16.0)[None, :, None] / 8).expand(c.T, 16, d).to(c.dt).contiguous()
+        for b in range(2):
+            n = c.hist_k[b].shape[0]
+            ramp = torch.linspace(0.0, 3.0, n) + (torch.arange(n) % 97 == 5) * 0.5
+            c.hist_k[b] = ramp[:, None, None].expand(n, 2, d).to(c.dt).contiguous()
+            for i in range(0, n, BLOCK):
+                m = min(BLOCK, n - i)
+                c.k_pool[c.table[b, i // BLOCK], :, :m] = c.hist_k[b][i:i + m].transpose(0, 1)
+        check(c, *attend(c), reference(c))
+
+
 @pytest.mark.parametrize("n_win", [0, 1, 128, 1280])
 @pytest.mark.parametrize("ns,ls", [([16], [5128]), ([16], [1288]), ([16, 1, 40], [136, 4000, 3720])])
 def test_tiles_that_end_a_block_apart(ns, ls, n_win):
@@ -644,13 +686,15 @@ def test_longest_lists():
     check(c, *select(c, idx, 1 << 30), reference(c, idx=idx, n_local=1 << 30))
 
 
-def test_selection_joined_in_windows():
+@pytest.mark.parametrize("ns", [[640], [2] * 20])
+def test_selection_joined_in_windows(ns):
     """Histories of more than 2048 blocks and so many items that a CTA's range
     of blocks passes 2048: the joined selection goes on in a second window.
     One block's K and V serve every table entry, so that only positions and
     masks tell; sampled tokens against the reference."""
     v = v4()
-    L, n, Hkv, d, n_sel = 2100 * BLOCK - 37, 640, 8, 64, 5
+    L, n, Hkv, d, n_sel = 2100 * BLOCK - 37, sum(ns), 8, 64, 5
+    start = np.concatenate([[0], np.cumsum(ns)])
     nb = -(-L // BLOCK)
     g = torch.Generator().manual_seed(4)
     kb = torch.randn(7, Hkv, BLOCK, d, generator=g).to(torch.float16)
@@ -665,13 +709,14 @@ def test_selection_joined_in_windows():
     lse = torch.empty(n, Hkv, device="cuda")
     v.block_sparse_attention(
         desc, q=q.cuda(), k_cache=kb.cuda(), v_cache=vb.cuda(), out=out, lse=lse, ws=ws,
-        q_start=torch.tensor([0, n], dtype=torch.int32, device="cuda"),
-        kv_len=torch.tensor([L], dtype=torch.int64, device="cuda"), block_table=table.cuda(),
+        q_start=torch.from_numpy(start).to(torch.int32).cuda(),
+        kv_len=torch.full((len(ns),), L, dtype=torch.int64, device="cuda"),
+        block_table=table.repeat(len(ns), 1).cuda(),
         idx=idx.cuda(), n_local=2)
     assert v.device_status(ws) == 0
     u = 2.0 ** -11
     for t in list(range(0, n, 37)) + [n - 1]:
-        p = L - n + t
+        p = L - int(start[start > t][0]) + t
         last = p // BLOCK
         blocks = sorted(set(idx[t].tolist()) | {last - 1, last})
         k = torch.cat([kb[table[0, b]][:, :(p % BLOCK + 1 if b == last else BLOCK)]
