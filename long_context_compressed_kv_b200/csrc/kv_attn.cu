@@ -34,8 +34,8 @@
 //     a softmax thread a key, P^T in shared memory.  The bytes bound these
 //     calls either way, but the MMAs' padding costs power and, under the power
 //     cap, clock: 32 steps of up to 16384 positions, after some seconds, take
-//     208 us at 1.34 GHz with M = 128, 192 at 1.58 with M = 64 on one card; 180 at
-//     1.75 with M = 64 and 172 at 1.96 turned on another.
+//     208 us at 1.34 GHz with M = 128, 192 at 1.58 with M = 64 and 179 turned on one
+//     card; 180 at 1.75 with M = 64 and 172 at 1.96 turned on another.
 // The MMA thread issues P V of one slot and the next Q K^T of the same slot
 // while the other slot's warps work on their scores.
 //
