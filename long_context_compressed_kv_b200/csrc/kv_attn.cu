@@ -526,7 +526,7 @@ struct Kernel {
                   ok = load_block(h, sp.lo + e + i, __shfl_sync(0xffffffffu, pb, i), 0xffffffffu);
               }
             } else {
-              ok = ok && sparse_piece(P, s, pc, e0, e1, lane, publish, load_block, page);
+              ok = ok && sparse_piece(P, s, pc, e0, e1, lane, publish, load_block, load_q, page);
             }
             ok = ok && load_q();
             ix = iend;
@@ -555,9 +555,9 @@ struct Kernel {
   // then its last blocks).  More: the blocks e0 .. e1-1 that any of them
   // selected, with a bit for each token that did, joined in shared memory
   // kWindow blocks at a time.
-  template <class Pub, class Load, class Page>
+  template <class Pub, class Load, class LoadQ, class Page>
   static __device__ bool sparse_piece(const KvAttnParams& P, S& s, Piece pc, int e0, int e1, int lane,
-                                      Pub& publish, Load& load_block, Page& page) {
+                                      Pub& publish, Load& load_block, LoadQ& load_q, Page& page) {
     const int li = P.n_lists > 1 ? pc.h : 0;
     auto list_of = [&](int tok) { return P.idx + ((int64_t)(pc.tok0 + tok) * P.n_lists + li) * P.n_sel; };
     // the warp's 32 entries from i0 on; good: they count, before: largest entry before them
@@ -659,6 +659,10 @@ struct Kernel {
           ok = load_block(pc.h, __shfl_sync(0xffffffffu, lb, i), __shfl_sync(0xffffffffu, pb, i),
                           __shfl_sync(0xffffffffu, mk, i));
       }
+      // A piece two windows on waits for this one's to be handed back, which takes
+      // the item's Q: asked for now, if fewer than two blocks were on their way.
+      // (It waits for the item before alone, all of whose blocks are.)
+      if (w1 < e1) ok = ok && load_q();
       w0 = w1;
     } while (ok && w0 < e1);
     return ok;

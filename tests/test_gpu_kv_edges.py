@@ -1,0 +1,68 @@
+"""16-bit K/V layers on the GPU, calls at the edges of what they admit: long
+histories with few blocks selected, values and starts out of the ordinary,
+against float64 references."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests.kv_util import BLOCK, counted
+from tests.test_gpu_kv import v4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.init()
+
+
+@pytest.mark.parametrize("ns", [[1280], [2] * 40])
+@pytest.mark.parametrize("early", ["none", "first", "one", "late"])
+def test_windows_that_hold_few_blocks(ns, early):
+    """More than a million positions, five windows of the joined selection, and
+    several items a CTA: items whose first windows hold no block or one (the
+    last blocks alone, the first and the last ones, one in the second window
+    for some tokens, entries of the last window) as chunks and as pairs of
+    tokens.  One pool block stands at every table entry but the last four, so
+    that a query's answer is that of a few keys with their numbers."""
+    v = v4()
+    nb, n, Hkv, d, n_local = 8300, sum(ns), 8, 64, 2
+    L = nb * BLOCK - 37
+    start = np.concatenate([[0], np.cumsum(ns)])
+    g = torch.Generator().manual_seed(len(early) + len(ns))
+    kb = torch.randn(5, Hkv, BLOCK, d, generator=g).to(torch.float16)
+    vb = torch.randn(5, Hkv, BLOCK, d, generator=g).to(torch.float16)
+    table = torch.zeros(1, nb, dtype=torch.int32)
+    table[0, -4:] = torch.arange(1, 5)
+    q = torch.randn(n, Hkv, d, generator=g).to(torch.float16)
+    idx = {"none": torch.empty(n, 1, 0), "first": torch.zeros(n, 1, 1),
+           "one": torch.where(torch.arange(n) % 32 == 5, 2100, -1)[:, None, None],
+           "late": torch.tensor([8195, nb - 4]).expand(n, 1, 2)}[early].to(torch.int32).contiguous()
+    desc = v.kv_desc(Hkv, Hkv, d, dtype=torch.float16)
+    ws = v.kv_workspace(desc)
+    out = torch.full((n, Hkv, d), 7.0, dtype=torch.float16, device="cuda")
+    lse = torch.full((n, Hkv), 7.0, device="cuda")
+    v.block_sparse_attention(
+        desc, q=q.cuda(), k_cache=kb.cuda(), v_cache=vb.cuda(), out=out, lse=lse, ws=ws,
+        q_start=torch.from_numpy(start).to(torch.int32).cuda(),
+        kv_len=torch.full((len(ns),), L, dtype=torch.int64, device="cuda"),
+        block_table=table.repeat(len(ns), 1).cuda(), idx=idx.cuda(), n_local=n_local)
+    assert v.device_status(ws) == 0
+    out, lse, u = out.double().cpu(), lse.double().cpu(), 2.0 ** -11
+    for t in [*range(0, n, 7 if n < 100 else 37), 5, n - 1]:
+        p = L - int(start[start > t][0]) + t
+        last = p // BLOCK
+        blocks = sorted(counted(idx[t, 0].tolist(), last) | {last - 1, last})
+        k, x = (torch.cat([pool[table[0, b]][:, :(p % BLOCK + 1 if b == last else BLOCK)]
+                           for b in blocks], 1).double() for pool in (kb, vb))
+        s = (k @ q[t].double()[:, :, None])[..., 0] / math.sqrt(d)
+        w, z = s.softmax(1), s.logsumexp(1)
+        want = (w[:, None] @ x)[:, 0]
+        e = d * 2.0 ** -23 * (k.abs() @ q[t].double().abs()[:, :, None]).amax(1) / math.sqrt(d)
+        tol = u * want.abs() + (u + 2 * (e + 2.0 ** -18)) * (w[:, None] @ x.abs())[:, 0] * (1 + u)
+        assert ((out[t] - want).abs() <= tol).all(), t
+        assert ((lse[t] - z).abs() <= e[:, 0] + 2.0 ** -18 + 2.0 ** -21 * (1 + z.abs())).all(), t
