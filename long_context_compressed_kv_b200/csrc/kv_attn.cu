@@ -128,9 +128,11 @@ struct Smem {
   Step step[2];                    // what the MMA thread says with each slot's scores
   Piece piece[2];
   float m1[MROWS], l1[MROWS];      // slot 1's statistics for the merge in the CTA
-  // turned items: what the four warps of a slot tell one another
+  // turned items: what the four warps of a slot tell one another, round by round
+  // (write, meet at xbar, read).  Two of each, taken in turn: a warp writes for
+  // round n + 2 once all have met in round n + 1, so have read what round n held.
   uint64_t xbar[2];
-  alignas(16) float xsum[2][4][kTurnedRows];
+  alignas(16) float xsum[2][2][4][kTurnedRows];
   alignas(4) uint8_t xflag[2][2][4];
   uint32_t tmem_base;
   uint32_t list_mask[SPARSE ? kWindow : 1];
@@ -1023,14 +1025,14 @@ struct Kernel {
             const float x = warp_max(v[c]);
             if (lane == c) w = x;
           }
-          if (lane < R) s.xsum[slot][wq][lane] = w;
+          float(*x)[R] = s.xsum[slot][nx & 1];
+          if (lane < R) x[wq][lane] = w;
           told();
           if (!met()) return false;
           float a[R];
 #pragma unroll
           for (int c = 0; c < R; ++c) {
-            const float mx = max3(fmaxf(s.xsum[slot][0][c], s.xsum[slot][1][c]), s.xsum[slot][2][c],
-                                  s.xsum[slot][3][c]);
+            const float mx = max3(fmaxf(x[0][c], x[1][c]), x[2][c], x[3][c]);
             const float mn = mx > m[c] + grow ? mx : m[c];
             a[c] = mx > m[c] + grow ? ex2((m[c] - mn) * sl2) : 1.0f;
             m[c] = mn;
@@ -1084,12 +1086,13 @@ struct Kernel {
         }
       }
       l[0] += __shfl_xor_sync(0xffffffffu, l[0], R);
-      if (lane < R) s.xsum[slot][wq][lane] = l[0];
+      float(*x)[R] = s.xsum[slot][nx & 1];
+      if (lane < R) x[wq][lane] = l[0];
       told();
 #pragma unroll
       for (int c = 0; c < R; ++c) mr = c0 == c ? m[c] : mr;
       if (!met()) return false;
-      lr = (s.xsum[slot][0][c0] + s.xsum[slot][1][c0]) + (s.xsum[slot][2][c0] + s.xsum[slot][3][c0]);
+      lr = (x[0][c0] + x[1][c0]) + (x[2][c0] + x[3][c0]);
     }
     auto release = [&]() {
       __syncwarp();

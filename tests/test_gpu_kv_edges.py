@@ -7,8 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.kv_util import BLOCK, counted
-from tests.test_gpu_kv import v4
+from tests.kv_util import BLOCK, Case, check, counted, reference
+from tests.test_gpu_kv import attend, v4
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,16 @@ def test_windows_that_hold_few_blocks(ns, early):
         tol = u * want.abs() + (u + 2 * (e + 2.0 ** -18)) * (w[:, None] @ x.abs())[:, 0] * (1 + u)
         assert ((out[t] - want).abs() <= tol).all(), t
         assert ((lse[t] - z).abs() <= e[:, 0] + 2.0 ** -18 + 2.0 ** -21 * (1 + z.abs())).all(), t
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,dtype,n", [(16, 2, 128, "bf16", 1), (8, 2, 64, "fp16", 3)])
+def test_many_short_steps_a_cta(Hq, Hkv, d, dtype, n):
+    """Decode steps of one to three blocks, eight and more items a CTA one after
+    the other: maxima and sums of one item are not taken for those of the next,
+    and ten runs give the same bits."""
+    rng = np.random.default_rng(d)
+    c = Case([n] * 600, [int(x) for x in rng.integers(n, 300, 600)], Hq, Hkv, d, dtype, seed=d)
+    first = attend(c)
+    check(c, *first, reference(c))
+    for _ in range(10):
+        assert all(torch.equal(x, y) for x, y in zip(first, attend(c)))
