@@ -1300,8 +1300,9 @@ struct Kernel {
           const float off = m == -INFINITY ? 0.f : m * sl2;
           const float sum = weights(v, sl2, off, t_s, keep ? 0xffffffffu : 0u, &s.pearly[slot]);
           l += SPARSE && !keep ? 0.f : sum;
-        } else if (lane == 0) {
-          mbar_arrive(&s.pearly[slot]);
+        } else {
+          __syncwarp();                                      // every lane's zeros before the word of them
+          if (lane == 0) mbar_arrive(&s.pearly[slot]);
         }
         if (active) tmem_st_wait();
         tc_fence_before();

@@ -79,3 +79,17 @@ def test_many_short_steps_a_cta(Hq, Hkv, d, dtype, n):
     check(c, *first, reference(c))
     for _ in range(10):
         assert all(torch.equal(x, y) for x, y in zip(first, attend(c)))
+
+
+@pytest.mark.parametrize("n_win", [0, 50])
+@pytest.mark.parametrize("ns,g,d", [([3], 8, 128), ([5, 2, 1], 6, 64), ([17, 18], 8, 128)])
+def test_warps_without_rows_clear_their_values(ns, g, d, n_win):
+    """Tiles whose rows leave some warps idle, on histories whose last block (and
+    with a window the first) is NaN past its end in every length of it: the
+    idle warps clear their share of V before the first products."""
+    for L in (133, 160, 161, 190, 200, 223, 255):
+        ls = [L + 7 * i for i in range(len(ns))]
+        c = Case(ns, ls, 4 * g, 4, d, seed=L)
+        for _ in range(5):
+            out, lse = attend(c, n_win)
+        check(c, out, lse, reference(c, n_win))
