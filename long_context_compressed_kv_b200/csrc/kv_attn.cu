@@ -205,9 +205,20 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
-// log of the denominator 2^top l; the sink itself, bit for bit, of a row without keys
+// Adds a head's sink to a row's sum l of weights in units of 2^top; returns the
+// factor of the weights so far.  Sinks beyond fp32 in the base of the
+// exponentials (inf and above 2.36e38) take all of the weight.
+__device__ __forceinline__ float join_sink(float sink, float& top, float& l) {
+  const float sk = sink * kLog2e, mm = fmaxf(top, sk), ms = mm == -INFINITY ? 0.f : mm;
+  const float f = ex2(top - ms);
+  l = l * f + (sk == ms ? 1.0f : ex2(sk - ms));
+  top = ms;
+  return f;
+}
+// log of the denominator 2^top l; the sink itself, bit for bit, of a row without
+// keys, and where the sink takes all
 __device__ __forceinline__ float log_sum(float top, float l, bool no_key, const float* sink, int h) {
-  if (no_key) return sink ? sink[h] : -INFINITY;
+  if (no_key || (sink && top == INFINITY && l == 1.0f)) return sink ? sink[h] : -INFINITY;
   return (top + log2f(l)) * kLn2;
 }
 // Registers a thread of the calling warpgroup may use from here on.
@@ -1134,12 +1145,7 @@ struct Kernel {
     float top = mr * sl2;
     if (part < 0) {
       float f = 1.0f;
-      if (P.sink && mine) {
-        const float sk = P.sink[hq] * kLog2e, mm = fmaxf(top, sk), ms = mm == -INFINITY ? 0.f : mm;
-        f = ex2(top - ms);
-        lr = lr * f + ex2(sk - ms);
-        top = ms;
-      }
+      if (P.sink && mine) f = join_sink(P.sink[hq], top, lr);
       f = lr == 0.f ? 0.f : f / lr;
       f0 *= f;
       f1 *= f;
@@ -1346,12 +1352,7 @@ struct Kernel {
       float top = m * sl2, f = 1.0f;                         // log2 of the largest weight
       if (part < 0) {
         const int hq = pc.h * P.g + rh;
-        if (P.sink && valid) {
-          const float sk = P.sink[hq] * kLog2e, mm = fmaxf(top, sk), ms = mm == -INFINITY ? 0.f : mm;
-          f = ex2(top - ms);
-          l = l * f + ex2(sk - ms);
-          top = ms;
-        }
+        if (P.sink && valid) f = join_sink(P.sink[hq], top, l);
         if (valid && P.lse)
           P.lse[(int64_t)(pc.tok0 + tok) * P.Hq + hq] = log_sum(top, l, m == -INFINITY, P.sink, hq);
         f = l == 0.f ? 0.f : f / l;
@@ -1563,13 +1564,8 @@ __global__ void __launch_bounds__(256) kv_merge_kernel(const __grid_constant__ K
     if (pl == 0 && i0 + rl < r.rows) {
       const int hq = r.h * P.g + hd;
       const bool none = top == -INFINITY;
-      float f = 1.0f, log_top = none ? 0.f : top;
-      if (P.sink) {
-        const float sk = P.sink[hq] * kLog2e, t2 = fmaxf(top, sk), z = t2 == -INFINITY ? 0.f : t2;
-        f = ex2(top - z);
-        l = l * f + ex2(sk - z);
-        log_top = z;
-      }
+      float f = 1.0f;
+      if (P.sink) f = join_sink(P.sink[hq], top, l);
       f = l == 0.f ? 0.f : f / l;
       uint4 w;
       w.x = pack16<F16>(x[0] * f, x[1] * f);
@@ -1580,7 +1576,7 @@ __global__ void __launch_bounds__(256) kv_merge_kernel(const __grid_constant__ K
                       (int64_t)(r.tok0 + tok) * P.out.tok + (int64_t)hq * P.out.head + d0;
       *reinterpret_cast<uint4*>(out) = w;
       if (P.lse && d0 == 0)
-        P.lse[(int64_t)(r.tok0 + tok) * P.Hq + hq] = log_sum(log_top, l, none, P.sink, hq);
+        P.lse[(int64_t)(r.tok0 + tok) * P.Hq + hq] = log_sum(top, l, none, P.sink, hq);
     }
   }
 }

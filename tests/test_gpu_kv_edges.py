@@ -7,8 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.kv_util import BLOCK, Case, check, counted, reference
-from tests.test_gpu_kv import attend, v4
+from tests.kv_util import BLOCK, ST_BAD_POSITION, Case, check, counted, reference
+from tests.test_gpu_kv import attend, select, v4
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,47 @@ def test_warps_without_rows_clear_their_values(ns, g, d, n_win):
         for _ in range(5):
             out, lse = attend(c, n_win)
         check(c, out, lse, reference(c, n_win))
+
+
+# new tokens, positions, heads, dim: items whole on a CTA (many sequences) and
+# cut over CTAs (few), of few rows and of many
+FORMS = [([1] * 400, [150] * 400, 16, 2, 128), ([30] * 200, [60] * 200, 8, 2, 64),
+         ([1, 2], [3000, 1500], 16, 2, 64), ([40], [1500], 8, 2, 128)]
+
+
+def forms(seed, dtype="bf16"):
+    """Each form's case, with calls of it over all keys and over every block as a selection."""
+    for ns, ls, Hq, Hkv, d in FORMS:
+        c = Case(ns, ls, Hq, Hkv, d, dtype, seed=seed)
+        m = max(ls) // BLOCK + 1
+        idx = torch.arange(m, dtype=torch.int32).expand(c.T, 1, m).contiguous()
+        yield c, (lambda sink=None, c=c: attend(c, sink=sink),
+                  lambda sink=None, c=c, idx=idx: select(c, idx, 0, sink))
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, 3.0e38, -3.0e38])
+def test_sinks_without_bounds(value):
+    """A sink of +inf takes all of a row's weight (out 0, lse inf), one of -inf
+    or near the type's lowest none, one near its largest all but nothing; the
+    other heads are as ever.  Rows without a key have the sink itself."""
+    for c, calls in forms(4):
+        sink = torch.randn(c.Hq, generator=torch.Generator().manual_seed(2))
+        want = list(reference(c, sink=sink))
+        sink[::3] = value
+        none = reference(c)
+        for call in calls:
+            out, lse = (x.cpu() for x in call(sink))
+            if value > 0:
+                assert (out[:, ::3] == 0).all()
+                # 2^-22: three roundings of fp32, to the base of the exponentials and back
+                assert (lse[:, ::3] == value).all() if value == math.inf else \
+                    ((lse[:, ::3] - value).abs() <= 2.0 ** -22 * value).all()
+                out[:, ::3], lse[:, ::3] = want[0][:, ::3].to(out.dtype), want[1][:, ::3].float()
+                check(c, out, lse, want)
+            else:
+                check(c, out, lse, [torch.where((torch.arange(c.Hq) % 3 > 0).view(
+                    -1, *[1] * (w.dim() - 2)), w, x) for w, x in zip(want, none)])
+    c = Case([3], [1], 8, 2, 64, seed=1)                     # positions -2, -1, 0
+    sink = torch.full((8,), value)
+    out, lse = attend(c, sink=sink, status=ST_BAD_POSITION)
+    assert (out[:2] == 0).all() and (lse[:2] == value).all()
