@@ -216,9 +216,11 @@ __device__ __forceinline__ float join_sink(float sink, float& top, float& l) {
   return f;
 }
 // log of the denominator 2^top l; the sink itself, bit for bit, of a row without
-// keys, and where the sink takes all
+// keys, and where the sink takes all.  A row that sees nothing but NaN has no
+// maximum either (maxima pass over NaN): its sum tells them apart.
 __device__ __forceinline__ float log_sum(float top, float l, bool no_key, const float* sink, int h) {
-  if (no_key || (sink && top == INFINITY && l == 1.0f)) return sink ? sink[h] : -INFINITY;
+  if ((no_key && l == l) || (sink && top == INFINITY && l == 1.0f))
+    return sink ? sink[h] : -INFINITY;
   return (top + log2f(l)) * kLn2;
 }
 // Registers a thread of the calling warpgroup may use from here on.

@@ -137,3 +137,20 @@ def test_sinks_without_bounds(value):
     sink = torch.full((8,), value)
     out, lse = attend(c, sink=sink, status=ST_BAD_POSITION)
     assert (out[:2] == 0).all() and (lse[:2] == value).all()
+
+
+@pytest.mark.parametrize("with_sink", [False, True])
+def test_nan_queries_show(with_sink):
+    """A query that is NaN has NaN as its output and as its log denominator (not
+    that of a query without keys); the others have their own."""
+    for c, calls in forms(3):
+        rng = np.random.default_rng(1)
+        bad = torch.from_numpy(rng.random((c.T, c.Hq)) < 0.2)
+        sink = torch.randn(c.Hq, generator=torch.Generator().manual_seed(2)) if with_sink else None
+        ref = reference(c, sink=sink)
+        c.q = torch.where(bad[..., None], math.nan, c.q)
+        for call in calls:
+            out, lse = (x.cpu() for x in call(sink))
+            assert out[bad].isnan().all() and lse[bad].isnan().all()
+            out[bad], lse[bad] = ref[0][bad].to(out.dtype), ref[1][bad].float()
+            check(c, out, lse, ref)
