@@ -699,7 +699,8 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (grp == 0) {
       const bool any = fin && Ms != -INFINITY;
       s.mg.rms[h] = any ? Ms : -INFINITY;
-      s.mg.rl[h] = any ? l : 0.f;
+      // (a row of NaN scores has no maximum, but its sum, and its O, are NaN)
+      s.mg.rl[h] = any || (fin && l != l) ? l : 0.f;
     }
   }
 
@@ -739,7 +740,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         tmem_ld_wait();
         // a split without keys has written no O: what the TMEM holds may be
         // anything of an earlier kernel, NaN too (which 0 would not clear)
-        if (!(lr > 0.f))
+        if (lr == 0.f)
 #pragma unroll
           for (int k = 0; k < 32; ++k) r[k] = 0;
         uint32_t hv[16];
@@ -849,7 +850,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (C == 1) {
       const float f = (M != -INFINITY && s.mg.rms[hh] != -INFINITY) ? ex2f(s.mg.rms[hh] - M) : 0.f;
       s.mg.fself[hh] = f;
-      den = f * s.mg.rl[hh];
+      den = f != 0.f ? f * s.mg.rl[hh] : 0.f;
     } else {
       for (int r = 0; r < C; ++r) {
         const float mr = fac[r * 128 + hh];
@@ -896,13 +897,14 @@ __global__ void __launch_bounds__(NTHR, 1)
       const int hh = quad * 32 + lane;
       const uint32_t ob = tmem + ((uint32_t)(quad * 32) << 16) + 256;
       const float f = s.mg.fself[hh];
+      const bool none = s.mg.rl[hh] == 0.f;
 #pragma unroll 1
       for (int cc = 0; cc < 256 / KG; cc += 32) {
         const int c = grp * (256 / KG) + cc;
         uint32_t r[32];
         tmem_ld32_nowait(ob + c, r);
         tmem_ld_wait();
-        if (f == 0.f)                                        // as above
+        if (none)                                            // as above
 #pragma unroll
           for (int k = 0; k < 32; ++k) r[k] = 0;
         if (row_h(hh) < P.H)
