@@ -331,8 +331,10 @@ v4attn_status v4attn_project(const v4attn_project_args* args, cudaStream_t strea
  * q_start[B]) are left as they were in every output.
  *
  * Checked by the kernels (status bit, the access skipped): a q_start that
- * decreases or leaves [0, T] (its sequence's rows are not taken); a position below 0 or past the block table (an
- * append leaves its token out, a query below 0 sees no key); a table entry
+ * decreases or leaves [0, T] (its sequence's rows are not taken, nor those of a
+ * later sequence that begins below a start before it: sequences taken share no
+ * row); a position below 0 or past the block table (an append leaves its token
+ * out, a query below 0 sees no key); a table entry
  * outside [0, n_blocks) (an append does not write, an attention does not see
  * the block's keys).  Two tokens of one call must not fall on the same cache
  * row (a block listed twice in the table): which one stays is not defined.

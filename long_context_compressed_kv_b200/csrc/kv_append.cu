@@ -101,15 +101,34 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(const __grid_constant__ K
     }
   };
   load(tid);
-  // the token's sequence: the number of sequences that end at or before it
-  int b = 0;
-  for (int i = 0; i < P.b.B; i += NT)
-    b += __syncthreads_count(i + tid < P.b.B && P.b.q_start[i + tid + 1] <= t);
+  // The token's sequence is the first that ends behind it; it is taken if it
+  // begins at or before the token and at no less than any start before it
+  // (sequences taken share no row, and no other can hold the token).
+  __shared__ int least[NT / 32], most[NT / 32];
+  int b = P.b.B;
+  bool bad = false;
+  for (int i = tid; i < P.b.B; i += NT) {
+    const int s0 = P.b.q_start[i], s1 = P.b.q_start[i + 1];
+    if (s1 > t) b = min(b, i);
+    bad = bad || s0 < 0 || s1 < s0 || s1 > P.b.T;
+  }
+  b = __reduce_min_sync(0xffffffffu, b);
+  if ((tid & 31) == 0) least[tid / 32] = b;
+  bad = __syncthreads_or(bad);
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) b = min(b, least[i]);
+  if (bad && t == 0 && tid == 0) flag(P.b.status, ST_BAD_SEQ);
   if (b >= P.b.B) return;
   const int q0 = P.b.q_start[b], q1 = P.b.q_start[b + 1];
-  if (t < q0 || q0 < 0 || q1 > P.b.T) {
-    if ((b > 0 || t >= q0) && tid == 0) flag(P.b.status, ST_BAD_SEQ);
-    return;
+  if (t < q0) return;
+  if (bad) {
+    int top = q0;
+    for (int i = tid; i < b; i += NT) top = max(top, P.b.q_start[i]);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((tid & 31) == 0) most[tid / 32] = top;
+    __syncthreads();
+    for (int i = 0; i < NT / 32; ++i) top = max(top, most[i]);
+    if (q0 < 0 || q1 > P.b.T || top > q0) return;
   }
   const int64_t p = P.b.kv_len[b] - (q1 - q0) + (t - q0);
   if (p < 0 || p >= (int64_t)P.b.bps * kKvBlock) {

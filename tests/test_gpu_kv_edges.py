@@ -7,8 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.kv_util import BLOCK, ST_BAD_POSITION, Case, check, counted, reference
-from tests.test_gpu_kv import attend, select, v4
+from tests.kv_util import BLOCK, ST_BAD_POSITION, ST_BAD_SEQ, Case, check, counted, reference
+from tests.test_gpu_kv import attend, desc_of, outputs, select, v4
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +154,70 @@ def test_nan_queries_show(with_sink):
             assert out[bad].isnan().all() and lse[bad].isnan().all()
             out[bad], lse[bad] = ref[0][bad].to(out.dtype), ref[1][bad].float()
             check(c, out, lse, ref)
+
+
+def taken(start, T):
+    """The sequences whose rows a call takes, by the header's rule."""
+    return [b for b, (x, y) in enumerate(zip(start, start[1:]))
+            if 0 <= x <= y <= T and x >= max(start[:b + 1])]
+
+
+@pytest.mark.parametrize("start", [
+    [0, 8, 4, 12], [0, 4, 8, 1000], [-3, 4, 8, 12], [0, 20, 8, 12], [5, 3, 4, 9], [2, 6, 6, 5],
+    # more sequences than a warp looks at in one go, a fall in the second group
+    # that the third is past of, and one to the end
+    [*range(0, 40), 20, *range(21, 70)], [*range(0, 40), 3, *range(4, 70)]])
+def test_sequences_beside_a_start_that_falls(start):
+    """A q_start that decreases or leaves [0, T]: appends and attention take the
+    rows of the same sequences, each row at most once, and leave the others."""
+    v = v4()
+    T, B = max(12, max(start) if len(start) > 4 else 0), len(start) - 1
+    rows = [(t, b, t - start[b]) for b in taken(start, T) for t in range(start[b], start[b + 1])]
+    assert len({t for t, _, _ in rows}) == len(rows)
+    # a history of 130 positions before each sequence's tokens
+    ls = [130 + max(0, y - x) for x, y in zip(start, start[1:])]
+    c = Case([0] * B, ls, 8, 2, 64, seed=B, front=T)
+    c.tokens = lambda: ((t, b, 130 + i) for t, b, i in rows)
+    desc = desc_of(c, d_rope=0)
+    ws = v.kv_workspace(desc)
+    kw = c.args(ws)
+    kw["q_start"] = torch.tensor(start, dtype=torch.int32, device="cuda")
+    x = torch.randn(T, 2, 64, generator=torch.Generator().manual_seed(1)).to(c.dt)
+    want_k = c.k_pool.clone()
+    for t, b, i in rows:
+        p = 130 + i
+        want_k[c.table[b, p // BLOCK], :, p % BLOCK] = x[t]
+        c.hist_k[b][p] = c.hist_v[b][p] = x[t]
+    v.kv_append(desc, k=x.cuda(), v=x.cuda(), **kw)
+    assert v.device_status_code(ws)[1] & ST_BAD_SEQ
+    assert torch.equal(kw["k_cache"].cpu().view(torch.int16), want_k.view(torch.int16))
+    v.workspace_init(ws)
+    out, lse = outputs(c)
+    v.paged_attention(desc, q=c.q.cuda(), out=out, lse=lse, **kw)
+    assert v.device_status_code(ws)[1] & ST_BAD_SEQ
+    check(c, out, lse, reference(c))
+
+
+def test_append_to_thousands_of_sequences():
+    """More sequences than threads, some without tokens."""
+    v = v4()
+    rng = np.random.default_rng(0)
+    ns = rng.choice([0, 0, 1, 3], 3000)
+    start = np.concatenate([[2], 2 + np.cumsum(ns)]).astype(np.int32)
+    T, d = int(start[-1]) + 3, 64
+    table = torch.from_numpy(rng.permutation(3000).astype(np.int32))[:, None]
+    ls = ns + rng.integers(0, 100, 3000)
+    x = torch.randn(T, 1, d, generator=torch.Generator().manual_seed(1)).half()
+    kc = torch.zeros(3000, 1, BLOCK, d, dtype=torch.float16)
+    want = kc.clone()
+    for b in range(3000):
+        t = np.arange(start[b], start[b + 1])
+        want[table[b, 0], 0, ls[b] - ns[b]:ls[b]] = x[t, 0]
+    desc = v.kv_desc(1, 1, d, dtype=torch.float16, d_rope=0)
+    ws = v.kv_workspace(desc)
+    kc, vc = kc.cuda(), kc.cuda()
+    v.kv_append(desc, k=x.cuda(), v=x.cuda(), k_cache=kc, v_cache=vc, ws=ws,
+                q_start=torch.from_numpy(start).cuda(), kv_len=torch.from_numpy(ls).cuda(),
+                block_table=table.cuda())
+    assert v.device_status(ws) == 0
+    assert torch.equal(kc.cpu(), want) and torch.equal(vc.cpu(), want)
