@@ -157,11 +157,15 @@ v4attn_status v4attn_kv_append(const v4attn_kv_desc* desc, const v4attn_kv_appen
   P.v = rows(a->v, a->v_token_stride, a->v_head_stride);
   P.k_cache = a->k_cache;
   P.v_cache = a->v_cache;
-  // theta^(-2k/d_rope) by repeated products: 64 of them round by 7e-15 at most,
-  // 1e-8 rad at position 2^20
-  const double step = desc->d_rope ? pow((double)desc->rope_theta, -2.0 / desc->d_rope) : 0.0;
-  double f = 0.15915494309189533577;                     // 1 / (2 pi)
-  for (int k = 0; k < 64; ++k, f *= step) P.freq[k] = k < desc->d_rope / 2 ? f : 0.0;
+  // theta^(-2k/d_rope) by repeated products in long double: 64 of them, the
+  // logarithm's and the power's own roundings (64-bit mantissas) stay below
+  // 2^-55, so that a frequency carries its rounding to double and no more.  With
+  // that of its product with the position an angle is off by 2^-52 p: 2.4e-7 rad
+  // at the last of 2^30 positions (products in double: up to 4e-6).
+  const long double step =
+      desc->d_rope ? exp2l(log2l(desc->rope_theta) * (-2.0L / desc->d_rope)) : 0.0L;
+  long double f = 0.159154943091895335768883763372514362L;   // 1 / (2 pi)
+  for (int k = 0; k < 64; ++k, f *= step) P.freq[k] = k < desc->d_rope / 2 ? (double)f : 0.0;
   return cuda_status(launch_kv_append(P, stream));
 }
 

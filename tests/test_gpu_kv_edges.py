@@ -221,3 +221,40 @@ def test_append_to_thousands_of_sequences():
                 block_table=table.cuda())
     assert v.device_status(ws) == 0
     assert torch.equal(kc.cpu(), want) and torch.equal(vc.cpu(), want)
+
+
+@pytest.mark.parametrize("theta", [1.1450824737548828, 1.0380772352218628, 10000.0])
+@pytest.mark.parametrize("halves", [False, True])
+def test_angles_at_the_farthest_positions(theta, halves):
+    """Rotations at the last positions that a table can hold, of pairs that their
+    angle turns onto an axis: what is left of the first member shows the angle.
+    The angle is off by two roundings of its turns in double, 2^-52 p <= 2^-22,
+    and by 2^-21 with sine and products in fp32; the result by a rounding."""
+    v = v4()
+    d, bps, n = 128, 1 << 23, 3
+    L = bps * BLOCK
+    p = np.arange(L - n, L)[:, None].astype(np.longdouble)
+    k = np.arange(d // 2).astype(np.longdouble)
+    angle = p * np.longdouble(theta) ** (-2 * k / d)
+    cos, sin = np.cos(angle), np.sin(angle)
+    size = 8.0
+    a = torch.from_numpy((size * sin).astype(np.float64)).half()
+    b = torch.from_numpy((size * cos).astype(np.float64)).half()
+    lay = (lambda x, y: torch.cat((x, y), -1)) if halves else \
+        (lambda x, y: torch.stack((x, y), -1).flatten(-2))
+    x = lay(a, b)[:, None].contiguous()
+    A, B = a.double().numpy().astype(np.longdouble), b.double().numpy().astype(np.longdouble)
+    want = lay(*(torch.from_numpy(w.astype(np.float64)) for w in (A * cos - B * sin,
+                                                                  A * sin + B * cos)))
+    desc = v.kv_desc(1, 1, d, dtype=torch.float16, rope_theta=theta, rope_halves=halves)
+    ws = v.kv_workspace(desc)
+    table = torch.zeros(1, bps, dtype=torch.int32, device="cuda")
+    kc, vc = (torch.zeros(1, 1, BLOCK, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    q_out = torch.empty_like(x, device="cuda")
+    v.kv_append(desc, k=x.cuda(), v=x.cuda(), q=x.cuda(), q_out=q_out, k_cache=kc, v_cache=vc,
+                q_start=torch.tensor([0, n], dtype=torch.int32, device="cuda"), ws=ws,
+                kv_len=torch.tensor([L], device="cuda"), block_table=table)
+    assert v.device_status(ws) == 0
+    tol = 2.0 ** -11 * want.abs() + (2.0 ** -21 + 2.0 ** -22) * size * (1 + 2.0 ** -10)
+    for got in (q_out[:, 0], kc[0, 0, -n:]):
+        assert ((got.double().cpu() - want).abs() <= tol).all()
