@@ -325,7 +325,11 @@ def _kv_cache(d, Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table, ws)
 
 
 _KV_CALLS = {fn: (_abi.packed_call(fn), fmt.pack) for fn, fmt in _abi.PACKED.items()}
-_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# what torch.cuda asks, without its checks (1 us less a call); a torch without
+# CUDA has neither, and imports this package all the same
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _kv_call(fn, desc, dev, ws, stream, *values):
