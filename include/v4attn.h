@@ -383,7 +383,8 @@ typedef struct {
  *   out = sum_j exp(s_j) v_j / den,  lse = log den
  * A query that sees no key gets out = 0 and lse = sink_h (-inf without sinks).
  * q . k, the softmax and its sums are fp32; exp(s_j), less a row's common
- * factor, enters the product with v_j rounded to the cache's type.  How the keys
+ * factor, enters the product with v_j rounded to the cache's type (fp16: in
+ * steps of 2^-31 of the row's largest at the least).  How the keys
  * are cut over CTAs, and with it the order of the fp32 sums, depends on the
  * whole batch; the same call gives the same bits.  Rows past a sequence's kv_len, rows of blocks that
  * no query of a call sees and rows before the first window may hold anything;

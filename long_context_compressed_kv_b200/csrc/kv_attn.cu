@@ -5,11 +5,12 @@
 //
 // Mathematics: softmax(q K^T) V in one pass over the keys, 128 (a pool block)
 // at a time: S = Q K^T, running maximum m and sum l of each row,
-// P = exp2(s scale log2e - m), O = O 2^(m_old - m) + P V.  O is rescaled only
-// when m would grow by more than 2^8 (P stays below 2^8, within fp16).  S, m, l
-// and O are fp32; l sums P before its rounding.  P is rounded to the cache's
-// type, which the tensor core wants of both operands of P V: a weight is off by
-// half a step at most, as the output is by its own rounding.
+// P = 2^shift exp2(s scale log2e - m), O = O 2^(m_old - m) + P V.  O is rescaled
+// only when m would grow by more than 2^8.  S, m, l and O are fp32; l sums P
+// before its rounding.  P is rounded to the cache's type, which the tensor core
+// wants of both operands of P V: a weight is off by half a step at most, as the
+// output is by its own rounding.  The shift, the same for a row's weights and
+// their sum, places P in the type's range (see kShift).
 //
 // Bounds.  Decode steps: HBM, 8 (g = 8) FLOP a byte.  32 steps of up to 16384
 // positions, 64 heads on 8, d = 128: 172 us, 6.45 TB/s of K and V.  Chunks: the
@@ -75,6 +76,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 1853 us, 32 columns 1785, 64 1750, 96 1792.
 constexpr int kEarly = 64;
 constexpr float kGrow = 8.0f;                  // log2 of the growth that rescales O
+// log2 of a weight of 1.  fp16 ends at 2^-24: with P up to 2^(7 + 8) of 2^16 a
+// weight counts down to 2^-32 of the largest (unshifted, keys below 2^-25 added
+// to the sum but not to O: 900 of them behind one key 2^25.5 above were lost).
+// bf16 has fp32's range, and P up to 1 leaves O that of the values' sum.
+template <bool F16>
+constexpr float kShift = F16 ? 7.0f : -kGrow;
 // Cost of an item besides its blocks, in blocks (Q load, epilogue): 32 decode
 // steps of up to 16384 positions 189 us at 1, 183 at 2.
 constexpr int kItemCost = 2;
@@ -1071,7 +1078,7 @@ struct Kernel {
             const float mn = mx > m[c] + grow ? mx : m[c];
             a[c] = mx > m[c] + grow ? ex2((m[c] - mn) * sl2) : 1.0f;
             m[c] = mn;
-            off[c] = mn == -INFINITY ? 0.f : mn * sl2;
+            off[c] = mn == -INFINITY ? 0.f : fmaf(mn, sl2, -kShift<F16>);
             l[c] *= a[c];
             p[c] = ex2(fmaf(v[c], sl2, -off[c]));
           }
@@ -1155,7 +1162,7 @@ struct Kernel {
     for (int c = 0; c < R; ++c) o0[c] = o1[c] = 0;
     if (has_o) tmem_ld16_nowait(t_o, o0);
     if (has1) tmem_ld16_nowait(t_o + D, o1);
-    // the factors of the row's two sums, its largest weight's log2, its sum of weights
+    // the factors of the row's two sums, the log2 of a weight's unit, its sum of weights
     float f0 = 1.0f, f1 = 0.f;
     if (has1) {
       const float m1 = s.m1[c0], mm = fmaxf(mr, m1), ms = mm == -INFINITY ? 0.f : mm;
@@ -1166,7 +1173,7 @@ struct Kernel {
     }
     const int tok = pc.tok0 + c0 / P.g, hq = pc.h * P.g + c0 % P.g, part = pc.part;
     const bool mine = c0 < rows;
-    float top = mr * sl2;
+    float top = fmaf(mr, sl2, -kShift<F16>);
     if (part < 0) {
       float f = 1.0f;
       if (P.sink && mine) f = join_sink(P.sink[hq], top, lr);
@@ -1327,7 +1334,7 @@ struct Kernel {
               }
             }
           }
-          const float off = m == -INFINITY ? 0.f : m * sl2;
+          const float off = m == -INFINITY ? 0.f : fmaf(m, sl2, -kShift<F16>);
           const float sum = weights(v, sl2, off, t_s, keep ? 0xffffffffu : 0u, &s.pearly[slot]);
           l += SPARSE && !keep ? 0.f : sum;
         } else {
@@ -1373,7 +1380,7 @@ struct Kernel {
         has1 = __any_sync(0xffffffffu, has1);                // the same in every lane
       }
       const int part = pc.part;
-      float top = m * sl2, f = 1.0f;                         // log2 of the largest weight
+      float top = fmaf(m, sl2, -kShift<F16>), f = 1.0f;      // log2 of a weight's unit
       if (part < 0) {
         const int hq = pc.h * P.g + rh;
         if (P.sink && valid) f = join_sink(P.sink[hq], top, l);

@@ -69,7 +69,7 @@ struct KvAttnParams {
   float* lse;
   int tt = 0;                         // tokens a tile (set at launch)
   // workspace: two parts a CTA (its first and last pieces), their rows'
-  // (log2 of the largest weight, sum of weights) and unnormalised outputs
+  // (log2 of a weight's unit, sum of weights) and unnormalised outputs
   KvPart* parts;                      // [kKvMaxCtas][2]
   float2* part_ml;                    // [kKvMaxCtas][2][kKvPartRows]
   float* part_o;                      // [kKvMaxCtas][2][kKvPartRows][d]

@@ -258,3 +258,44 @@ def test_angles_at_the_farthest_positions(theta, halves):
     tol = 2.0 ** -11 * want.abs() + (2.0 ** -21 + 2.0 ** -22) * size * (1 + 2.0 ** -10)
     for got in (q_out[:, 0], kc[0, 0, -n:]):
         assert ((got.double().cpu() - want).abs() <= tol).all()
+
+
+def first_keys_apart(c, n, logit, other_v):
+    """Keys whose logits are 0 but for the first n of each sequence, at ``logit``,
+    with values 0 there and ``other_v`` (1 + j / 512) elsewhere."""
+    q = 1.0
+    c.q = torch.full_like(c.q, q)
+    for b, x in enumerate(c.ls):
+        c.hist_k[b] = torch.zeros_like(c.hist_k[b])
+        c.hist_k[b][:n] = logit / (q * math.sqrt(c.d))
+        v = other_v * (1 + (torch.arange(x) % 512) / 512.0)
+        v[:n] = 0.0
+        c.hist_v[b] = v[:, None, None].expand(x, c.Hkv, c.d).to(c.dt).contiguous()
+        for i in range(0, x, BLOCK):
+            m = min(BLOCK, x - i)
+            for pool, hist in ((c.k_pool, c.hist_k), (c.v_pool, c.hist_v)):
+                pool[c.table[b, i // BLOCK], :, :m] = hist[b][i:i + m].transpose(0, 1)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("ns,ls,Hq,Hkv,d", [([1] * 160, [900] * 160, 16, 2, 64),
+                                            ([30] * 60, [700] * 60, 8, 2, 64),
+                                            ([1], [20000], 8, 1, 128)])
+def test_many_keys_far_below_one(ns, ls, Hq, Hkv, d, dtype):
+    """One key e^17.7 = 2^25.5 above all others, whose values are what the output
+    holds: weights that small still count."""
+    c = Case(ns, ls, Hq, Hkv, d, dtype, seed=1, spare=0)
+    first_keys_apart(c, 1, 17.7, 64.0)
+    check(c, *attend(c), reference(c))
+    idx = torch.arange(-(-max(ls) // BLOCK), dtype=torch.int32).expand(c.T, 1, -1).contiguous()
+    check(c, *select(c, idx, 0), reference(c))
+
+
+@pytest.mark.parametrize("ns,ls,Hq,Hkv,d", [([1] * 160, [300] * 160, 16, 2, 64),
+                                            ([30] * 60, [300] * 60, 8, 2, 64)])
+def test_large_values(ns, ls, Hq, Hkv, d):
+    """bf16 values whose sum, weights up to 1, fits fp32, behind logits that rise
+    by less than what moves the running maximum."""
+    c = Case(ns, ls, Hq, Hkv, d, "bf16", seed=1, spare=0)
+    first_keys_apart(c, BLOCK, -5.0, 5e35)
+    check(c, *attend(c), reference(c))
