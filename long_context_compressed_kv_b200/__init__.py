@@ -307,6 +307,8 @@ def _kv_cache(d, Hkv, dtype, k_cache, v_cache, q_start, kv_len, block_table, ws)
             or kv_len.get_device() != dev or block_table.get_device() != dev
             or ws.get_device() != dev):
         raise ValueError("k_cache, v_cache, q_start, kv_len, block_table and ws must live on one GPU")
+    if not ws.is_contiguous():         # its bytes are counted from its shape
+        raise ValueError("ws must be contiguous")
     if (H != Hkv or rows != 128 or dims != d or v_cache.shape != pool or k_cache.dtype is not dtype
             or v_cache.dtype is not dtype or not k_cache.is_contiguous()
             or not v_cache.is_contiguous()):

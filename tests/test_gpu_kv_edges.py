@@ -299,3 +299,21 @@ def test_large_values(ns, ls, Hq, Hkv, d):
     c = Case(ns, ls, Hq, Hkv, d, "bf16", seed=1, spare=0)
     first_keys_apart(c, BLOCK, -5.0, 5e35)
     check(c, *attend(c), reference(c))
+
+
+def test_workspaces_that_are_no_memory():
+    """An expanded tensor has a workspace's size in its shape alone: refused."""
+    v = v4()
+    c = Case([1], [300], 8, 2, 64, seed=1)
+    desc = desc_of(c)
+    n = v.kv_workspace(desc).numel()
+    for ws in (torch.zeros(1, dtype=torch.uint8, device="cuda").expand(n),
+               torch.zeros(2, n, dtype=torch.uint8, device="cuda")[:, ::2]):
+        args = c.args(ws)
+        out, lse = outputs(c)
+        x = torch.zeros(1, 2, 64, dtype=c.dt, device="cuda")
+        with pytest.raises(ValueError, match="contiguous"):
+            v.paged_attention(desc, q=c.q.cuda(), out=out, lse=lse, **args)
+        with pytest.raises(ValueError, match="contiguous"):
+            v.kv_append(desc, k=x, v=x, **args)
+        assert (out == 7.0).all() and (lse == 7.0).all()
