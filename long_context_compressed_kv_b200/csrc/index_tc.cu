@@ -530,7 +530,12 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// Encoding wants a current context, which a host thread that has made no
+// runtime call but cudaGetDevice yet lacks: its device is set (to what it is) once.
 static EncodeTiledFn encode_fn() {
+  static thread_local bool ready = false;
+  int dev = 0;
+  if (!ready) ready = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
   static EncodeTiledFn fn = nullptr;
   if (!fn) {
     void* p = nullptr;
