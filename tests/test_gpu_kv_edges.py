@@ -2,6 +2,8 @@
 histories with few blocks selected, values and starts out of the ordinary,
 against float64 references."""
 import math
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -317,3 +319,51 @@ def test_workspaces_that_are_no_memory():
         with pytest.raises(ValueError, match="contiguous"):
             v.kv_append(desc, k=x, v=x, **args)
         assert (out == 7.0).all() and (lse == 7.0).all()
+
+
+FIRST_CALL = """
+import torch
+from tests.kv_util import Case, check, reference
+import long_context_compressed_kv_b200 as v
+c = Case([20, 1], [300, 200], 8, 2, 64, seed=9)
+desc = v.kv_desc(8, 2, 64, d_rope=0)
+ws = v.kv_workspace(desc)
+kw = c.args(ws)
+q, out, lse = c.q.cuda(), torch.empty(c.T, 8, 64, dtype=c.dt, device="cuda"), torch.empty(c.T, 8, device="cuda")
+new = [torch.cat([h[b][L - n:] for b, (n, L) in enumerate(zip(c.ns, c.ls))]).cuda()
+       for h in (c.hist_k, c.hist_v)]
+lists = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda").expand(c.T, 2).contiguous()
+side = torch.cuda.Stream()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    # a copy and a kernel on two streams, both waited for by the first call
+    start = torch.cuda.current_stream()
+    side.wait_stream(start)
+    with torch.cuda.stream(side):
+        kv = [x.clone() for x in new]
+    q2 = q + 0
+    lens = kw["kv_len"] * 1
+    start.wait_stream(side)
+    kw["kv_len"] = lens
+    v.kv_append(desc, k=kv[0], v=kv[1], **kw)
+    if SPARSE:
+        v.block_sparse_attention(desc, q=q2, out=out, lse=lse, idx=lists, n_local=1, **kw)
+    else:
+        v.paged_attention(desc, q=q2, out=out, lse=lse, **kw)
+    again = out * 2
+for _ in range(3):
+    out.zero_()
+    graph.replay()
+assert v.device_status(ws) == 0
+check(c, out, lse, reference(c, idx=lists.cpu()[:, None] if SPARSE else None, n_local=1))
+assert torch.equal(again, out * 2)
+"""
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_first_calls_of_a_process_captured(sparse):
+    """The first calls of a process are captured, behind a copy and a kernel of two
+    streams and in front of one."""
+    p = subprocess.run([sys.executable, "-c", f"SPARSE = {sparse}\n" + FIRST_CALL],
+                       capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
