@@ -367,3 +367,31 @@ def test_first_calls_of_a_process_captured(sparse):
     p = subprocess.run([sys.executable, "-c", f"SPARSE = {sparse}\n" + FIRST_CALL],
                        capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stderr[-2000:]
+
+
+def test_rows_far_apart():
+    """Token rows 2^30 elements apart: the third begins past 2^31."""
+    v = v4()
+    c = Case([2, 1], [300, 140], 8, 2, 64, seed=2)
+    new = [torch.cat([h[b][L - n:] for b, (n, L) in enumerate(zip(c.ns, c.ls))])
+           for h in (c.hist_k, c.hist_v)]
+    wide = torch.empty((2 << 30) + 20 * 64, dtype=c.dt, device="cuda")
+
+    def heads(first, n):
+        return wide[first * 64:].as_strided((3, n, 64), (1 << 30, 64, 1))
+
+    q, k, x, out = heads(0, 8), heads(8, 2), heads(10, 2), heads(12, 8)
+    for dst, src in ((q, c.q), (k, new[0]), (x, new[1])):
+        dst.copy_(src)
+    out.fill_(7.0)
+    desc = desc_of(c, d_rope=0)
+    ws = v.kv_workspace(desc)
+    kw = c.args(ws)
+    before = [kw[n].cpu().view(torch.int16) for n in ("k_cache", "v_cache")]
+    v.kv_append(desc, k=k, v=x, q=q, q_out=q, **kw)
+    lse = torch.empty(3, 8, device="cuda")
+    v.paged_attention(desc, q=q, out=out, lse=lse, **kw)
+    assert v.device_status(ws) == 0
+    assert all(torch.equal(kw[n].cpu().view(torch.int16), b)
+               for n, b in zip(("k_cache", "v_cache"), before))
+    check(c, out, lse, reference(c))
