@@ -13,11 +13,14 @@
 // their sum, places P in the type's range (see kShift).
 //
 // Bounds.  Decode steps: HBM, 8 (g = 8) FLOP a byte.  32 steps of up to 16384
-// positions, 64 heads on 8, d = 128: 172 us, 6.45 TB/s of K and V.  Chunks: the
-// tensor pipe (2 x 1024 of its cycles a block and pair of tiles), short of that
-// the chain scores -> P -> P V -> next scores of a slot, which the other slot's
-// half hides: 2048 tokens on 32768: 1.75 ms, 1.2 PFLOP/s, pipe 59% busy.  Short
-// calls: launch, work list, first load and merge, about 10 us.
+// positions, 64 heads on 8, d = 128: 172 to 180 us by the card, 6.16 to 6.45 TB/s
+// of K and V.  Chunks: the tensor pipe (2 x 1024 of its cycles a block and pair of
+// tiles), short of that the chain scores -> P -> P V -> next scores of a slot,
+// which the other slot's half hides: 2048 tokens on 32768 after some seconds, under
+// the power cap: 2.0 to 2.1 ms, 1.04 PFLOP/s (first launches 1.74 ms, 1.22
+// PFLOP/s, pipe 64% busy).  At d = 64 the exponentials (16 a cycle and SM) take
+// longer than the tensor pipe.  Short calls: launch, work list, first load and
+// merge, about 10 us.
 //
 // Rows.  The g = Hq / Hkv query heads that share a K/V head are rows of one
 // tile: row r is token r / g, head r % g, tt = 128 / g tokens a tile.  An item
