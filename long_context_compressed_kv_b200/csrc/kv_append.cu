@@ -101,52 +101,85 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(const __grid_constant__ K
     }
   };
   load(tid);
-  // The token's sequence is the first that ends behind it; it is taken if it
-  // begins at or before the token and at no less than any start before it
-  // (sequences taken share no row, and no other can hold the token).
-  __shared__ int least[NT / 32], most[NT / 32];
-  int b = P.b.B;
+  // The token's sequence: the number of sequences that end at or before it,
+  // where starts do not fall.  Whether they do comes with the barrier below.
+  int b = 0;
   bool bad = false;
   for (int i = tid; i < P.b.B; i += NT) {
     const int s0 = P.b.q_start[i], s1 = P.b.q_start[i + 1];
-    if (s1 > t) b = min(b, i);
+    b += s1 <= t;
     bad = bad || s0 < 0 || s1 < s0 || s1 > P.b.T;
   }
-  b = __reduce_min_sync(0xffffffffu, b);
-  if ((tid & 31) == 0) least[tid / 32] = b;
-  bad = __syncthreads_or(bad);
-#pragma unroll
-  for (int i = 0; i < NT / 32; ++i) b = min(b, least[i]);
-  if (bad && t == 0 && tid == 0) flag(P.b.status, ST_BAD_SEQ);
-  if (b >= P.b.B) return;
-  const int q0 = P.b.q_start[b], q1 = P.b.q_start[b + 1];
-  if (t < q0) return;
-  if (bad) {
-    int top = q0;
-    for (int i = tid; i < b; i += NT) top = max(top, P.b.q_start[i]);
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((tid & 31) == 0) most[tid / 32] = top;
+  if (P.b.B <= NT) {
+    b = __syncthreads_count(b);
+  } else {
+    __shared__ int part[NT / 32];
+    b = __reduce_add_sync(0xffffffffu, b);
+    if ((tid & 31) == 0) part[tid / 32] = b;
     __syncthreads();
-    for (int i = 0; i < NT / 32; ++i) top = max(top, most[i]);
-    if (q0 < 0 || q1 > P.b.T || top > q0) return;
+    b = 0;
+    for (int i = 0; i < NT / 32; ++i) b += part[i];
   }
-  const int64_t p = P.b.kv_len[b] - (q1 - q0) + (t - q0);
-  if (p < 0 || p >= (int64_t)P.b.bps * kKvBlock) {
-    if (tid == 0) flag(P.b.status, ST_BAD_POSITION);
-    return;
+  // its position and pool block; false: it belongs to no sequence
+  int64_t p;
+  int32_t blk;
+  bool page;
+  uint32_t wrong;
+  auto find = [&]() -> bool {
+    wrong = 0;
+    if (b >= P.b.B) return false;
+    if (t < P.b.q_start[b]) return false;
+    p = P.b.kv_len[b] - P.b.q_start[b + 1] + t;
+    if (p < 0 || p >= (int64_t)P.b.bps * kKvBlock) {
+      wrong = ST_BAD_POSITION;
+      return false;
+    }
+    blk = P.b.bt[(int64_t)b * P.b.bps + p / kKvBlock];
+    page = blk >= 0 && blk < P.b.n_blocks;
+    if (!page) wrong = ST_BAD_INDEX;
+    return true;
+  };
+  bool mine = find();
+  auto turn = [&]() {
+    if (mine && tid < half) {
+      // turns in double, reduced to half a turn either way before going to float
+      double r = (double)p * P.freq[tid];
+      r -= rint(r);
+      float co, si;
+      sincospif(2.0f * (float)r, &si, &co);
+      cs[tid] = make_float2(co, si);
+    }
+  };
+  turn();
+  if (__syncthreads_or(bad)) {
+    // Some start falls or leaves [0, T].  The token's sequence is the first that
+    // ends behind it; it is taken if it begins at or before the token and at no
+    // less than any start before it (sequences taken share no row, and no other
+    // can hold the token).
+    __shared__ int first, most;
+    if (tid == 0) {
+      first = P.b.B;
+      most = 0;
+    }
+    __syncthreads();
+    wrong = 0;
+    int low = P.b.B;
+    for (int i = tid; i < P.b.B; i += NT)
+      if (P.b.q_start[i + 1] > t) low = min(low, i);
+    if (low < P.b.B) atomicMin(&first, low);
+    __syncthreads();
+    b = first;
+    int top = 0;
+    for (int i = tid; i <= b && i < P.b.B; i += NT) top = max(top, P.b.q_start[i]);
+    if (top > 0) atomicMax(&most, top);
+    __syncthreads();
+    mine = b < P.b.B && P.b.q_start[b] >= most && P.b.q_start[b + 1] <= P.b.T && find();
+    turn();
+    if (t == 0 && tid == 0) flag(P.b.status, ST_BAD_SEQ);
+    __syncthreads();
   }
-  const int32_t blk = P.b.bt[(int64_t)b * P.b.bps + p / kKvBlock];
-  const bool page = blk >= 0 && blk < P.b.n_blocks;
-  if (!page && tid == 0) flag(P.b.status, ST_BAD_INDEX);
-  if (tid < half) {
-    // turns in double, reduced to half a turn either way before going to float
-    double r = (double)p * P.freq[tid];
-    r -= rint(r);
-    float co, si;
-    sincospif(2.0f * (float)r, &si, &co);
-    cs[tid] = make_float2(co, si);
-  }
-  __syncthreads();
+  if (wrong && tid == 0) flag(P.b.status, wrong);
+  if (!mine) return;
   for (int i0 = tid; i0 < n; i0 += NB * NT) {
     if (i0 != tid) load(i0);
 #pragma unroll
