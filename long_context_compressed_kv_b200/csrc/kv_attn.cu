@@ -265,10 +265,11 @@ struct SeqInfo {
   int len;           // positions with keys: kv_len cut to the table
 };
 
-__device__ __forceinline__ SeqInfo seq_info(const KvAttnParams& P, int b, bool report, int& q1) {
+// fall: the sequence ends below its start
+__device__ __forceinline__ SeqInfo seq_info(const KvAttnParams& P, int b, bool report, bool& fall) {
   SeqInfo s;
-  const int q0 = P.b.q_start[b];
-  q1 = P.b.q_start[b + 1];
+  const int q0 = P.b.q_start[b], q1 = P.b.q_start[b + 1];
+  fall = q1 < q0;
   const int64_t len = P.b.kv_len[b], cap = (int64_t)P.b.bps * NK;
   const bool bad = q0 < 0 || q1 < q0 || q1 > P.b.T;
   s.q0 = q0;
@@ -326,38 +327,37 @@ __device__ __forceinline__ SeqInfo shfl_seq(const SeqInfo& s, int src) {
   return r;
 }
 
+// After a start that falls: does sequence b0 + lane, which begins at q0, begin
+// below one before it?  Such are left out, so that sequences taken share no row.
+// (Out of line: the common path keeps its registers.)
+__device__ __noinline__ bool begins_below(const KvBatch& b, int b0, int q0, int lane) {
+  int top = 0;
+  for (int i = lane; i < b0; i += 32) top = max(top, b.q_start[i]);
+  top = __reduce_max_sync(0xffffffffu, top);
+  int m = b0 + lane < b.B ? b.q_start[b0 + lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, m, o);
+    if (lane >= o) m = max(m, v);
+  }
+  return q0 < max(m, top);
+}
+
 // The warp's place in the laid-out work: walks (sequence, head, item).
 struct Walk {
   int b0;            // sequences b0 .. b0+31, one a lane
   SeqInfo mine;      // this lane's sequence
   int64_t head;      // cost of one head of this lane's sequence
   int per_item;
-  int top;           // the largest start so far
+  bool falls = false;   // a start before this group's end is below the one before it
 
-  // The group of sequences from `first` on (0, then 32 further each time).
   __device__ __forceinline__ void load(const KvAttnParams& P, int first, int lane, bool report) {
     b0 = first;
-    if (first == 0) top = 0;
     mine = SeqInfo{0, 0, 0, 0};
-    int q0 = 0x7FFFFFFF, q1 = q0;
-    if (b0 + lane < P.b.B) {
-      mine = seq_info(P, b0 + lane, report, q1);
-      q0 = mine.q0;
-    }
-    // after a start that decreases, sequences that begin below one before are
-    // left out too: those taken share no row
-    if (__any_sync(0xffffffffu, q1 < q0 || q0 < top)) {
-      int m = b0 + lane < P.b.B ? q0 : top;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, m, o);
-        if (lane >= o) m = max(m, v);
-      }
-      if (q0 < max(m, top)) mine.n = 0;
-      top = max(top, __shfl_sync(0xffffffffu, m, 31));
-    } else {
-      top = __shfl_sync(0xffffffffu, b0 + 31 < P.b.B ? q0 : top, 31);
-    }
+    bool fall = false;
+    if (b0 + lane < P.b.B) mine = seq_info(P, b0 + lane, report, fall);
+    falls = __any_sync(0xffffffffu, fall) || falls;
+    if (falls && begins_below(P.b, b0, mine.q0, lane)) mine.n = 0;
     head = 0;
     if (mine.n > 0 && mine.n <= per_item) head = item_span(P, mine, 0, mine.n).n + kItemCost;
     unsigned many = __ballot_sync(0xffffffffu, mine.n > per_item);
