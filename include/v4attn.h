@@ -382,7 +382,8 @@ typedef struct {
  *   s_j = softmax_scale q . k_j,  den = exp(sink_h) + sum_j exp(s_j)
  *   out = sum_j exp(s_j) v_j / den,  lse = log den
  * A query that sees no key gets out = 0 and lse = sink_h (-inf without sinks).
- * q . k, the softmax and its sums are fp32; exp(s_j), less a row's common
+ * q . k, the softmax and its sums are fp32 (the tensor core's of at most 256
+ * blocks at a time, which it cuts off by 2^-12 at most); exp(s_j), less a row's common
  * factor, enters the product with v_j rounded to the cache's type (fp16: in
  * steps of 2^-31 of the row's largest at the least).  How the keys
  * are cut over CTAs, and with it the order of the fp32 sums, depends on the
@@ -407,9 +408,9 @@ typedef struct {
   float* lse;                 /* device [T][Hq] or NULL */
 } v4attn_kv_attn_args;
 
-/* Bytes of workspace for calls on this layer, of any size (43 MB at d = 128, for
- * the parts of queries whose keys are split over SMs); 0 for a layer that is
- * refused.  Zero its header with v4attn_workspace_init before the first
+/* Bytes of workspace for calls on this layer, of any size (64 MB at d = 128, for
+ * the parts of queries whose keys are split over SMs and the sums over long
+ * histories); 0 for a layer that is refused.  Zero its header with v4attn_workspace_init before the first
  * call; one workspace serves one stream at a time (two captured graphs may
  * share it when their replays are ordered). */
 size_t v4attn_kv_workspace_size(const v4attn_kv_desc* desc);

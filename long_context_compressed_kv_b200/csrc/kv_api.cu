@@ -9,11 +9,13 @@ using namespace v4a;
 
 namespace {
 
-// Workspace: [status header | parts | their statistics | their outputs]
+// Workspace: [status header | parts | their statistics | the sums' maxima | the
+// parts' outputs | the sums]
 constexpr size_t kPartsOff = sizeof(WsHeader);
 constexpr size_t kMlOff = kPartsOff + sizeof(KvPart) * 2 * kKvMaxCtas;
-constexpr size_t kOutOff = kMlOff + sizeof(float2) * 2 * kKvMaxCtas * kKvPartRows;
-static_assert(kMlOff % 16 == 0 && kOutOff % 16 == 0, "workspace alignment");
+constexpr size_t kFoldMOff = kMlOff + sizeof(float2) * 2 * kKvMaxCtas * kKvPartRows;
+constexpr size_t kOutOff = kFoldMOff + sizeof(float) * kKvMaxCtas * kKvPartRows;
+static_assert(kMlOff % 16 == 0 && kFoldMOff % 16 == 0 && kOutOff % 16 == 0, "workspace alignment");
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -116,6 +118,8 @@ v4attn_status run_attention(const v4attn_kv_desc* d, const v4attn_kv_attn_args* 
   P.parts = reinterpret_cast<KvPart*>(w8 + kPartsOff);
   P.part_ml = reinterpret_cast<float2*>(w8 + kMlOff);
   P.part_o = reinterpret_cast<float*>(w8 + kOutOff);
+  P.fold_m = reinterpret_cast<float*>(w8 + kFoldMOff);
+  P.fold_o = reinterpret_cast<float4*>(P.part_o + (size_t)2 * kKvMaxCtas * kKvPartRows * d->d);
   return cuda_status(launch_kv_attn(P, st));
 }
 
@@ -125,7 +129,7 @@ extern "C" {
 
 size_t v4attn_kv_workspace_size(const v4attn_kv_desc* desc) {
   if (check_kv_desc(desc) != V4A_OK) return 0;
-  return kOutOff + sizeof(float) * 2 * kKvMaxCtas * kKvPartRows * desc->d;
+  return kOutOff + sizeof(float) * 3 * kKvMaxCtas * kKvPartRows * desc->d;
 }
 
 v4attn_status v4attn_kv_append(const v4attn_kv_desc* desc, const v4attn_kv_append_args* a, void* ws,

@@ -85,6 +85,12 @@ constexpr float kGrow = 8.0f;                  // log2 of the growth that rescal
 // bf16 has fp32's range, and P up to 1 leaves O that of the values' sum.
 template <bool F16>
 constexpr float kShift = F16 ? 7.0f : -kGrow;
+// Blocks that a slot's O takes up in one go.  The tensor core adds to its fp32
+// sums by cutting off, up to 2^-23 of them each 16 keys: with values of one sign
+// O loses 2^-20.3 of itself a block, and 4096 blocks in a slot (160 decode steps on
+// 2^20 positions) made it 0.34% too small.  After kFold blocks O is added to a sum
+// outside the tensor core, and begins again: 2^-12 at most, 2^-12.3 measured.
+constexpr int kFold = 256;
 // Cost of an item besides its blocks, in blocks (Q load, epilogue): 32 decode
 // steps of up to 16384 positions 189 us at 1, 183 at 2.
 constexpr int kItemCost = 2;
@@ -160,6 +166,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// to += from, or to = from: 16 columns of fp32
+__device__ __forceinline__ void add16(uint32_t to, uint32_t from, bool add) {
+  uint32_t a[16], b[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) b[e] = 0;
+  tmem_ld16_nowait(from, a);
+  if (add) tmem_ld16_nowait(to, b);
+  tmem_ld_wait();
+#pragma unroll
+  for (int e = 0; e < 16; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) + __uint_as_float(b[e]));
+  tmem_st16(to, a);
+  tmem_st_wait();
 }
 // MMA whose A operand (P) is read from tensor memory: M = 128 rows at lanes
 // 0..127, two 16-bit elements of K a column
@@ -372,7 +391,7 @@ struct Walk {
 
 // ---------------------------------------------------------------- kernel
 
-template <int D, bool F16, bool SPARSE, bool TURN>
+template <int D, bool F16, bool SPARSE, bool TURN, bool LONG>
 struct Kernel {
   using S = Smem<D, SPARSE>;
   using C = Cfg<D, SPARSE>;
@@ -742,7 +761,7 @@ struct Kernel {
     };
     const uint32_t q_at = smem_u32(s.q) >> 4, kv_at = smem_u32(s.kv) >> 4;
     int base = 0, items = 0, np[2] = {0, 0}, ne[2] = {0, 0}, pend[2] = {-1, -1};
-    uint32_t acc[2] = {0, 0};
+    uint32_t acc[2] = {0, 0};                              // blocks that a slot has taken
     auto wait_tile = [&](int i) { return mbar_wait_at(&s.full[i % NST], (i / NST) & 1, status, 3); };
     // turned: P^T is a B operand in shared memory, in the place of the second Q tile:
     // 32 bytes (16 rows) a key, 16-byte halves exchanged in every other four keys
@@ -758,6 +777,9 @@ struct Kernel {
         mma_f16(TM_S + slot * NK, a + off, b + off, id_qk(form), kk > 0);
       }
     };
+    // does O hold blocks already?
+    auto begun = [&](int slot) -> uint32_t { return LONG ? acc[slot] % kFold : acc[slot]; };
+    auto taken = [&](int slot) { acc[slot] = LONG ? acc[slot] + 1 : 1; };
     auto pv = [&](int slot, int tile, bool rest, int form) {
       tc_fence_after();
       const uint64_t b = v_bits | (kv_at + tile % NST * (C::kTile / 16));
@@ -765,8 +787,8 @@ struct Kernel {
       for (int kk = 0; kk < NK / 16; ++kk)        // 16 keys: 8 columns of P, 16 rows x 128 bytes
         if ((kk >= kEarly / 16) == rest)
           mma_f16_ts(TM_O + slot * D, TM_S + slot * NK + 8 * kk, b + 128 * kk, id_pv(form),
-                 kk > 0 ? 1u : acc[slot]);
-      if (rest) acc[slot] = 1;
+                 kk > 0 ? 1u : begun(slot));
+      if (rest) taken(slot);
     };
     auto qk_turned = [&](int slot, int tile) {
       tc_fence_after();
@@ -786,8 +808,8 @@ struct Kernel {
 #pragma unroll
       for (int kk = 0; kk < NK / 16; ++kk)
         mma_f16(TM_O + slot * D, a + 128 * kk, b + 32 * kk,
-                idesc_f(fmt, fmt, D, kTurnedRows, true, true), kk > 0 ? 1u : acc[slot]);
-      acc[slot] = 1;
+                idesc_f(fmt, fmt, D, kTurnedRows, true, true), kk > 0 ? 1u : begun(slot));
+      taken(slot);
     };
     // A slot's warps answer each step on pready: with P, or, where there were no
     // scores, that they have read the step (open: the answer is outstanding).
@@ -980,6 +1002,8 @@ struct Kernel {
       l[c] = 0.f;
     }
     bool has_o = false;
+    int nb = 0;                                  // blocks of the item seen
+    const uint32_t t_sum = t_s + 2 * R;          // O of earlier runs of kFold blocks
     // the four warps' writes before are seen by all behind it
     auto met = [&]() -> bool {
       const bool ok = mbar_wait_warp(&s.xbar[slot], nx & 1, status, 12);
@@ -999,116 +1023,135 @@ struct Kernel {
       const int all_hi = min(pc.pos0, pc.len - 1);
       const int all_lo = P.n_win ? pc.pos0 + pc.ntok - P.n_win : (int)0x80000000;
       const int lane_tok = min(lane / P.g, 31);
-      for (;;) {
-        if (!mbar_wait_warp(&s.sready[slot], ns & 1, status, 8)) return false;
-        ++ns;
-        const Step stp = s.step[slot];
-        tc_fence_after();
-        if (stp.tile < 0) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.pready[slot]);
-          break;
+      bool end = false;
+      do {                                         // runs of kFold blocks
+        if (LONG && nb > 0 && nb % kFold == 0) {
+          // P V of the run's last block is complete when the next scores are there
+          if (!mbar_wait_warp(&s.sready[slot], ns & 1, status, 8)) return false;
+          tc_fence_after();
+          if (s.step[slot].tile >= 0) add16(t_sum, t_o, nb > kFold);
         }
-        float v[R], p[R];
-        {
-          uint32_t raw[R];
-          tmem_ld16_nowait(t_s, raw);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < R; ++c) v[c] = __uint_as_float(raw[c]);
-        }
-        const int blk = stp.blk, kb = blk * NK, key = kb + r;
-        if (blk >= 0 && (kb + NK > vhi || kb < vlo)) {
-          // V rows that nobody sees are zeroed, as below
-          const int st = stp.tile % NST;
-          if (!mbar_wait_warp(&s.full[st], (stp.tile / NST) & 1, status, 9)) return false;
-          if (key >= vhi || key < vlo) {
-            const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4*>(s.kv[st] + c * (MROWS * 128) + r * 128 + e * 16) = z;
+        for (;;) {
+          if (!mbar_wait_warp(&s.sready[slot], ns & 1, status, 8)) return false;
+          ++ns;
+          const Step stp = s.step[slot];
+          tc_fence_after();
+          if (stp.tile < 0) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.pready[slot]);
+            end = true;
+            break;
           }
-        }
-        // rows that see this thread's key, a bit each: tokens from `from` on, to `to`
-        uint32_t vis = 0xffff;
-        if (blk < 0 || kb + NK - 1 > all_hi || kb < all_lo) {
-          const int from = min(max(key - pc.pos0, 0), R) * P.g;
-          vis = blk < 0 || key >= pc.len ? 0 : vis << min(from, R);
-          if (P.n_win) {
-            const int to = min(max(key - pc.pos0 + P.n_win, 0), R) * P.g;
-            vis &= (1u << min(to, R)) - 1;
-          }
-          vis &= 0xffff;
-        }
-        if (SPARSE) vis &= __ballot_sync(0xffffffffu, (stp.mask >> lane_tok) & 1);
-        if (__any_sync(0xffffffffu, vis != 0xffff)) {
-#pragma unroll
-          for (int c = 0; c < R; ++c) v[c] = vis >> c & 1 ? v[c] : -INFINITY;
-        }
-        // Does a maximum grow?  A first block's do.
-        bool grows = !has_o;
-        if (has_o) {
-          bool up = false;
-#pragma unroll
-          for (int c = 0; c < R; ++c) up = up || v[c] > m[c] + grow;
-          up = __any_sync(0xffffffffu, up);
-          if (lane == 0) s.xflag[slot][nx & 1][wq] = up;
-          told();
-          // the weights as if none did, while the other warps' word comes
-#pragma unroll
-          for (int c = 0; c < R; ++c) p[c] = ex2(fmaf(v[c], sl2, -off[c]));
-          const uint32_t* flags = reinterpret_cast<const uint32_t*>(s.xflag[slot][nx & 1]);
-          if (!met()) return false;
-          grows = *flags != 0;
-        }
-        if (grows) {
-          float w = 0.f;
-#pragma unroll
-          for (int c = 0; c < R; ++c) {
-            const float x = warp_max(v[c]);
-            if (lane == c) w = x;
-          }
-          float(*x)[R] = s.xsum[slot][nx & 1];
-          if (lane < R) x[wq][lane] = w;
-          told();
-          if (!met()) return false;
-          float a[R];
-#pragma unroll
-          for (int c = 0; c < R; ++c) {
-            const float mx = max3(fmaxf(x[0][c], x[1][c]), x[2][c], x[3][c]);
-            const float mn = mx > m[c] + grow ? mx : m[c];
-            a[c] = mx > m[c] + grow ? ex2((m[c] - mn) * sl2) : 1.0f;
-            m[c] = mn;
-            off[c] = mn == -INFINITY ? 0.f : fmaf(mn, sl2, -kShift<F16>);
-            l[c] *= a[c];
-            p[c] = ex2(fmaf(v[c], sl2, -off[c]));
-          }
-          if (has_o) {
-            // P V of the block before is complete: its commit came with these scores
-            uint32_t o[R];
-            tmem_ld16_nowait(t_o, o);
+          float v[R], p[R];
+          {
+            uint32_t raw[R];
+            tmem_ld16_nowait(t_s, raw);
             tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < R; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * a[c]);
-            tmem_st16(t_o, o);
-            tmem_st_wait();
+            for (int c = 0; c < R; ++c) v[c] = __uint_as_float(raw[c]);
           }
+          const int blk = stp.blk, kb = blk * NK, key = kb + r;
+          if (blk >= 0 && (kb + NK > vhi || kb < vlo)) {
+            // V rows that nobody sees are zeroed, as below
+            const int st = stp.tile % NST;
+            if (!mbar_wait_warp(&s.full[st], (stp.tile / NST) & 1, status, 9)) return false;
+            if (key >= vhi || key < vlo) {
+              const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  *reinterpret_cast<uint4*>(s.kv[st] + c * (MROWS * 128) + r * 128 + e * 16) = z;
+            }
+          }
+          // rows that see this thread's key, a bit each: tokens from `from` on, to `to`
+          uint32_t vis = 0xffff;
+          if (blk < 0 || kb + NK - 1 > all_hi || kb < all_lo) {
+            const int from = min(max(key - pc.pos0, 0), R) * P.g;
+            vis = blk < 0 || key >= pc.len ? 0 : vis << min(from, R);
+            if (P.n_win) {
+              const int to = min(max(key - pc.pos0 + P.n_win, 0), R) * P.g;
+              vis &= (1u << min(to, R)) - 1;
+            }
+            vis &= 0xffff;
+          }
+          if (SPARSE) vis &= __ballot_sync(0xffffffffu, (stp.mask >> lane_tok) & 1);
+          if (__any_sync(0xffffffffu, vis != 0xffff)) {
+#pragma unroll
+            for (int c = 0; c < R; ++c) v[c] = vis >> c & 1 ? v[c] : -INFINITY;
+          }
+          // Does a maximum grow?  A first block's do.
+          bool grows = !has_o;
+          if (has_o) {
+            bool up = false;
+#pragma unroll
+            for (int c = 0; c < R; ++c) up = up || v[c] > m[c] + grow;
+            up = __any_sync(0xffffffffu, up);
+            if (lane == 0) s.xflag[slot][nx & 1][wq] = up;
+            told();
+            // the weights as if none did, while the other warps' word comes
+#pragma unroll
+            for (int c = 0; c < R; ++c) p[c] = ex2(fmaf(v[c], sl2, -off[c]));
+            const uint32_t* flags = reinterpret_cast<const uint32_t*>(s.xflag[slot][nx & 1]);
+            if (!met()) return false;
+            grows = *flags != 0;
+          }
+          if (grows) {
+            float w = 0.f;
+#pragma unroll
+            for (int c = 0; c < R; ++c) {
+              const float x = warp_max(v[c]);
+              if (lane == c) w = x;
+            }
+            float(*x)[R] = s.xsum[slot][nx & 1];
+            if (lane < R) x[wq][lane] = w;
+            told();
+            if (!met()) return false;
+            float a[R];
+#pragma unroll
+            for (int c = 0; c < R; ++c) {
+              const float mx = max3(fmaxf(x[0][c], x[1][c]), x[2][c], x[3][c]);
+              const float mn = mx > m[c] + grow ? mx : m[c];
+              a[c] = mx > m[c] + grow ? ex2((m[c] - mn) * sl2) : 1.0f;
+              m[c] = mn;
+              off[c] = mn == -INFINITY ? 0.f : fmaf(mn, sl2, -kShift<F16>);
+              l[c] *= a[c];
+              p[c] = ex2(fmaf(v[c], sl2, -off[c]));
+            }
+            if (has_o) {
+              // P V of the block before is complete: its commit came with these scores
+              uint32_t o[R];
+              tmem_ld16_nowait(t_o, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < R; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * a[c]);
+              tmem_st16(t_o, o);
+              tmem_st_wait();
+              if (LONG && nb >= kFold) {
+                tmem_ld16_nowait(t_sum, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < R; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * a[c]);
+                tmem_st16(t_sum, o);
+                tmem_st_wait();
+              }
+            }
+          }
+          uint32_t pk[R / 2];
+#pragma unroll
+          for (int c = 0; c < R; ++c) l[c] += p[c];
+#pragma unroll
+          for (int c = 0; c < R; c += 2) pk[c / 2] = pack16<F16>(p[c], p[c + 1]);
+          *reinterpret_cast<uint4*>(pt + swap) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          *reinterpret_cast<uint4*>(pt + (swap ^ 16)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.pready[slot]);
+          has_o = true;
+          if (LONG && ++nb % kFold == 0) break;
         }
-        uint32_t pk[R / 2];
-#pragma unroll
-        for (int c = 0; c < R; ++c) l[c] += p[c];
-#pragma unroll
-        for (int c = 0; c < R; c += 2) pk[c / 2] = pack16<F16>(p[c], p[c + 1]);
-        *reinterpret_cast<uint4*>(pt + swap) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        *reinterpret_cast<uint4*>(pt + (swap ^ 16)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.pready[slot]);
-        has_o = true;
-      }
+      } while (LONG && !end);
       if (pc.last) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.pempty[pi]);
@@ -1119,6 +1162,7 @@ struct Kernel {
     const Piece& pc = s.piece[pieces & 1];
     const int c0 = lane & (R - 1);
     float mr = -INFINITY, lr = 0.f;
+    if (LONG && nb > kFold) add16(t_o, t_sum, true);
     if (has_o) {
       // sums over the warp's lanes, halving the rows a lane holds each time
 #pragma unroll
@@ -1227,6 +1271,7 @@ struct Kernel {
     wait_grid();
     float m = -INFINITY, l = 0.f;
     bool has_o = false;
+    int nb = 0;                                              // blocks of the item seen
     for (int pieces = 0;; ++pieces) {
       const int pi = pieces & 1;
       if (!mbar_wait_warp(&s.pfull[pi], (pieces >> 1) & 1, status, 7)) return;
@@ -1255,101 +1300,160 @@ struct Kernel {
       const int all_hi = __reduce_min_sync(0xffffffffu, hi), all_lo = __reduce_max_sync(0xffffffffu, lo);
       // rows of V that no query of the item sees: before its first window, past its end
       const int vlo = P.n_win ? pc.pos0 - P.n_win + 1 : 0, vhi = pc.len;
+      // The row's O to its sum over earlier runs (or, at the item's end, that sum to
+      // O), each in units of the maximum that it was formed with.  The sums of a
+      // slot's rows lie in the workspace, four dims of all of them side by side.
+      auto fold = [&](bool end) {
+        const int own = (int)blockIdx.x * 2 + slot, at = own * MROWS + (row & (MROWS - 1));
+        float4* sum = P.fold_o + (int64_t)own * MROWS * (D / 4) + (row & (MROWS - 1));
+        const bool more = valid && nb > kFold;
+        const float was = more ? P.fold_m[at] : -INFINITY;
+        const float f = was == -INFINITY ? 0.f : ex2((was - m) * sl2);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          float4 w[8];
+          tmem_ld32_nowait(t_o + c, o);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            w[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (more) w[e] = sum[(c / 4 + e) * MROWS];
+          }
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            w[e].x = fmaf(w[e].x, f, __uint_as_float(o[4 * e]));
+            w[e].y = fmaf(w[e].y, f, __uint_as_float(o[4 * e + 1]));
+            w[e].z = fmaf(w[e].z, f, __uint_as_float(o[4 * e + 2]));
+            w[e].w = fmaf(w[e].w, f, __uint_as_float(o[4 * e + 3]));
+          }
+          if (end) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              o[4 * e] = __float_as_uint(w[e].x);
+              o[4 * e + 1] = __float_as_uint(w[e].y);
+              o[4 * e + 2] = __float_as_uint(w[e].z);
+              o[4 * e + 3] = __float_as_uint(w[e].w);
+            }
+            tmem_st16(t_o + c, o);
+            tmem_st16(t_o + c + 16, o + 16);
+          } else if (valid) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[(c / 4 + e) * MROWS] = w[e];
+          }
+          __syncwarp();
+        }
+        if (end) tmem_st_wait();
+        if (valid && !end) P.fold_m[at] = m;
+      };
       if (pc.first) {
         m = -INFINITY;
         l = 0.f;
         has_o = false;
+        nb = 0;
       }
-      for (;;) {
-        if (!mbar_wait_warp(&s.sready[slot], ns & 1, status, 8)) return;
-        ++ns;
-        const Step stp = s.step[slot];
-        tc_fence_after();
-        if (stp.tile < 0) {                                  // the last P V is complete
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.pready[slot]);
-          break;
+      bool end = false;
+      do {                                                   // runs of kFold blocks
+        if (LONG && nb > 0 && nb % kFold == 0) {
+          // P V of the run's last block is complete when the next scores are there
+          if (!mbar_wait_warp(&s.sready[slot], ns & 1, status, 8)) return;
+          tc_fence_after();
+          if (active && s.step[slot].tile >= 0) fold(false);
         }
-        const int blk = stp.blk, kb = blk * NK;
-        if (blk >= 0 && (kb + NK > vhi || kb < vlo)) {
-          // V rows that nobody sees may hold anything, and 0 x NaN is NaN: zero them
-          const int key = kb + r, st = stp.tile % NST;
-          if (!mbar_wait_warp(&s.full[st], (stp.tile / NST) & 1, status, 9)) return;
-          if (key >= vhi || key < vlo) {
-            const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4*>(s.kv[st] + c * (MROWS * 128) + r * 128 + e * 16) = z;
+        for (;;) {
+          if (!mbar_wait_warp(&s.sready[slot], ns & 1, status, 8)) return;
+          ++ns;
+          const Step stp = s.step[slot];
+          tc_fence_after();
+          if (stp.tile < 0) {                                  // the last P V is complete
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.pready[slot]);
+            end = true;
+            break;
           }
-          fence_proxy_async_smem();
-        }
-        if (active) {
-          float v[NK];
-          {
-            uint32_t raw[NK];
+          const int blk = stp.blk, kb = blk * NK;
+          if (blk >= 0 && (kb + NK > vhi || kb < vlo)) {
+            // V rows that nobody sees may hold anything, and 0 x NaN is NaN: zero them
+            const int key = kb + r, st = stp.tile % NST;
+            if (!mbar_wait_warp(&s.full[st], (stp.tile / NST) & 1, status, 9)) return;
+            if (key >= vhi || key < vlo) {
+              const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int c = 0; c < NK; c += 32) tmem_ld32_nowait(t_s + c, raw + c);
-            tmem_ld_wait();
+              for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-            for (int c = 0; c < NK; ++c) v[c] = __uint_as_float(raw[c]);
+                for (int e = 0; e < 8; ++e)
+                  *reinterpret_cast<uint4*>(s.kv[st] + c * (MROWS * 128) + r * 128 + e * 16) = z;
+            }
+            fence_proxy_async_smem();
           }
-          // columns lc .. hc are seen; keep: the row's token takes the block
-          const bool keep = blk >= 0 && (!SPARSE || !valid || ((stp.mask >> tok) & 1));
-          const int hc = blk < 0 ? -1 : hi - kb, lc = lo == (int)0x80000000 ? 0 : lo - kb;
-          if (blk < 0 || kb + NK - 1 > all_hi) {
+          if (active) {
+            float v[NK];
+            {
+              uint32_t raw[NK];
 #pragma unroll
-            for (int c = 0; c < NK; ++c) v[c] = c <= hc ? v[c] : -INFINITY;
-          }
-          if (!SPARSE && kb < all_lo) {
+              for (int c = 0; c < NK; c += 32) tmem_ld32_nowait(t_s + c, raw + c);
+              tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < NK; ++c) v[c] = c >= lc ? v[c] : -INFINITY;
-          }
-          float x[4];
+              for (int c = 0; c < NK; ++c) v[c] = __uint_as_float(raw[c]);
+            }
+            // columns lc .. hc are seen; keep: the row's token takes the block
+            const bool keep = blk >= 0 && (!SPARSE || !valid || ((stp.mask >> tok) & 1));
+            const int hc = blk < 0 ? -1 : hi - kb, lc = lo == (int)0x80000000 ? 0 : lo - kb;
+            if (blk < 0 || kb + NK - 1 > all_hi) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[c] = v[c];
+              for (int c = 0; c < NK; ++c) v[c] = c <= hc ? v[c] : -INFINITY;
+            }
+            if (!SPARSE && kb < all_lo) {
 #pragma unroll
-          for (int c = 4; c < NK - 4; c += 8) {
+              for (int c = 0; c < NK; ++c) v[c] = c >= lc ? v[c] : -INFINITY;
+            }
+            float x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = max3(x[e], v[c + 2 * e], v[c + 2 * e + 1]);
-          }
+            for (int c = 0; c < 4; ++c) x[c] = v[c];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[c] = max3(x[c], v[NK - 4 + c], x[c]);
-          float mx = max3(max3(x[0], x[1], x[2]), x[3], x[3]);
-          if (SPARSE && !keep) mx = -INFINITY;
-          const bool up = mx > m + grow;
-          if (__any_sync(0xffffffffu, up)) {
-            const float mn = up ? mx : m;
-            const float a = up ? ex2((m - mn) * sl2) : 1.0f;
-            m = mn;
-            l *= a;
-            if (has_o) {
-              // P V of the block before is complete: its commit came with these scores
+            for (int c = 4; c < NK - 4; c += 8) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = max3(x[e], v[c + 2 * e], v[c + 2 * e + 1]);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[c] = max3(x[c], v[NK - 4 + c], x[c]);
+            float mx = max3(max3(x[0], x[1], x[2]), x[3], x[3]);
+            if (SPARSE && !keep) mx = -INFINITY;
+            const bool up = mx > m + grow;
+            if (__any_sync(0xffffffffu, up)) {
+              const float mn = up ? mx : m;
+              const float a = up ? ex2((m - mn) * sl2) : 1.0f;
+              m = mn;
+              l *= a;
+              if (has_o) {
+                // P V of the block before is complete: its commit came with these scores
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tmem_ld16_nowait(t_o + c, o);
-                tmem_ld_wait();
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16_nowait(t_o + c, o);
+                  tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                tmem_st16(t_o + c, o);
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                  tmem_st16(t_o + c, o);
+                }
               }
             }
+            const float off = m == -INFINITY ? 0.f : fmaf(m, sl2, -kShift<F16>);
+            const float sum = weights(v, sl2, off, t_s, keep ? 0xffffffffu : 0u, &s.pearly[slot]);
+            l += SPARSE && !keep ? 0.f : sum;
+          } else {
+            __syncwarp();                                      // every lane's zeros before the word of them
+            if (lane == 0) mbar_arrive(&s.pearly[slot]);
           }
-          const float off = m == -INFINITY ? 0.f : fmaf(m, sl2, -kShift<F16>);
-          const float sum = weights(v, sl2, off, t_s, keep ? 0xffffffffu : 0u, &s.pearly[slot]);
-          l += SPARSE && !keep ? 0.f : sum;
-        } else {
-          __syncwarp();                                      // every lane's zeros before the word of them
-          if (lane == 0) mbar_arrive(&s.pearly[slot]);
+          if (active) tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.pready[slot]);
+          has_o = true;
+          if (LONG && ++nb % kFold == 0) break;
         }
-        if (active) tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.pready[slot]);
-        has_o = true;
-      }
+      } while (LONG && !end);
+      if (LONG && pc.last && active && nb > kFold) fold(true);
       if (!pc.last) {
         release();
         continue;
@@ -1446,12 +1550,12 @@ struct Kernel {
 
 }  // namespace
 
-template <int D, bool F16, bool SPARSE, bool TURN>
+template <int D, bool F16, bool SPARSE, bool TURN, bool LONG>
 __global__ void __launch_bounds__(NTHREADS, 1)
     kv_attn_kernel(const __grid_constant__ KvAttnParams P, const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v) {
-  using K = Kernel<D, F16, SPARSE, TURN>;
+  using K = Kernel<D, F16, SPARSE, TURN, LONG>;
   using S = typename K::S;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>(smem_raw);
@@ -1624,7 +1728,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-template <int D, bool F16, bool SPARSE, bool TURN>
+template <int D, bool F16, bool SPARSE, bool TURN, bool LONG>
 cudaError_t launch(const KvAttnParams& P, const CUtensorMap& q, const CUtensorMap& k,
                    const CUtensorMap& v, int grid, int dev, cudaStream_t st) {
   const size_t smem = sizeof(Smem<D, SPARSE>);
@@ -1632,7 +1736,7 @@ cudaError_t launch(const KvAttnParams& P, const CUtensorMap& q, const CUtensorMa
   static unsigned long long configured = 0;
   if (dev >= 64 || !(configured & (1ull << dev))) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kv_attn_kernel<D, F16, SPARSE, TURN>,
+        cudaFuncSetAttribute(kv_attn_kernel<D, F16, SPARSE, TURN, LONG>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) configured |= 1ull << dev;
@@ -1647,13 +1751,25 @@ cudaError_t launch(const KvAttnParams& P, const CUtensorMap& q, const CUtensorMa
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, F16, SPARSE, TURN>, P, q, k, v);
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, F16, SPARSE, TURN, LONG>, P, q, k, v);
   if (e != cudaSuccess) return e;
   // rows of an item: at most two tiles, at most the call's tokens
   cfg.gridDim = dim3(grid, std::min(16, std::min(P.b.T, 2 * P.tt) * P.g), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, F16>, P, grid);
+}
+
+// The most blocks that a slot can be given of an item: those of the table, of the
+// windows of an item's tokens, or those that they can select; half of them where
+// no item has two tiles (and a window of a joined selection one more).
+int64_t most_blocks(const KvAttnParams& P) {
+  const int64_t tokens = std::min(P.b.T, 2 * P.tt);
+  int64_t n = P.b.bps;
+  if (P.n_win) n = std::min<int64_t>(n, (P.n_win + tokens - 2) / NK + 2);
+  if (P.sparse) n = std::min<int64_t>(n, tokens * ((int64_t)P.n_sel + P.n_local));
+  return P.b.T <= P.tt ? (n + P.b.bps / kWindow + 2) / 2 : n;
 }
 
 }  // namespace
@@ -1698,13 +1814,23 @@ cudaError_t launch_kv_attn(const KvAttnParams& params, cudaStream_t st) {
   // 32768 would take 1755 us there, 1725 on the other; a mixed batch of 9
   // sequences 53.3 and 49.5.
   const bool turn = (int64_t)P.b.T * P.g <= (int64_t)P.b.B * kTurnedRows;
-#define KV_LAUNCH(D, F)                                                   \
-  (P.sparse ? turn ? launch<D, F, true, true>(P, mq, mk, mv, grid, dev, st)   \
-                   : launch<D, F, true, false>(P, mq, mk, mv, grid, dev, st)  \
-   : turn   ? launch<D, F, false, true>(P, mq, mk, mv, grid, dev, st)         \
-            : launch<D, F, false, false>(P, mq, mk, mv, grid, dev, st))
-  if (P.d == 128) return P.f16 ? KV_LAUNCH(128, true) : KV_LAUNCH(128, false);
-  return P.f16 ? KV_LAUNCH(64, true) : KV_LAUNCH(64, false);
+  // Calls that can give a slot more blocks than O takes up at once on the kernel
+  // that adds O up (2048 tokens on 131072: 9.53 ms without, 9.66 with; 32 steps of up
+  // to 131072 1.29 and 1.29; 64 steps on selected blocks 111.8 us and 113.7).  It is
+  // not the only one because of its other loop: a mixed batch of 9 sequences 51.3
+  // and 51.6 us, four prompts of up to 4096 450 and 457.
+  const bool many = most_blocks(P) > kFold;
+#define KV_LAUNCH(D, F, S)                                                    \
+  (turn ? many ? launch<D, F, S, true, true>(P, mq, mk, mv, grid, dev, st)    \
+               : launch<D, F, S, true, false>(P, mq, mk, mv, grid, dev, st)   \
+   : many ? launch<D, F, S, false, true>(P, mq, mk, mv, grid, dev, st)        \
+          : launch<D, F, S, false, false>(P, mq, mk, mv, grid, dev, st))
+  if (P.d == 128) {
+    if (P.sparse) return P.f16 ? KV_LAUNCH(128, true, true) : KV_LAUNCH(128, false, true);
+    return P.f16 ? KV_LAUNCH(128, true, false) : KV_LAUNCH(128, false, false);
+  }
+  if (P.sparse) return P.f16 ? KV_LAUNCH(64, true, true) : KV_LAUNCH(64, false, true);
+  return P.f16 ? KV_LAUNCH(64, true, false) : KV_LAUNCH(64, false, false);
 #undef KV_LAUNCH
 }
 

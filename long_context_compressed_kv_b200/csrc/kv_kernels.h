@@ -73,6 +73,10 @@ struct KvAttnParams {
   KvPart* parts;                      // [kKvMaxCtas][2]
   float2* part_ml;                    // [kKvMaxCtas][2][kKvPartRows]
   float* part_o;                      // [kKvMaxCtas][2][kKvPartRows][d]
+  // and, a CTA's own, its two slots' sums over an item's blocks so far and the
+  // maxima that these go with
+  float4* fold_o;                     // [kKvMaxCtas][2][d / 4][kKvPartRows / 2]
+  float* fold_m;                      // [kKvMaxCtas][2][kKvPartRows / 2]
 };
 
 cudaError_t launch_kv_append(const KvAppendParams& P, cudaStream_t st);

@@ -395,3 +395,61 @@ def test_rows_far_apart():
     assert all(torch.equal(kw[n].cpu().view(torch.int16), b)
                for n, b in zip(("k_cache", "v_cache"), before))
     check(c, out, lse, reference(c))
+
+
+@pytest.mark.parametrize("rising", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+# sequences, new tokens, positions, heads, dim: items of thousands of blocks on a
+# CTA, of 8, 32 and 100 rows and of two tiles
+@pytest.mark.parametrize("B,n,L,Hq,Hkv,d", [(160, 1, 1 << 19, 8, 1, 128), (150, 1, 1 << 19, 32, 1, 64),
+                                            (75, 1, 1 << 19, 200, 2, 64), (80, 40, 1 << 19, 8, 1, 128)])
+def test_sums_over_long_histories(B, n, L, Hq, Hkv, d, dtype, rising):
+    """Values of one sign over thousands of blocks on one CTA: the tensor core cuts
+    its sums off, by up to 2^-23 of them each 16 keys, for which the 256 blocks
+    that it takes in one go allow 2^-12.  The table's entries are seven pool blocks,
+    in an order in which logits rise or at random."""
+    v = v4()
+    nb, u = L // BLOCK, torch.finfo(dtype).eps / 2
+    g = torch.Generator().manual_seed(Hq)
+    kb = 0.3 * torch.randn(7, Hkv, BLOCK, d, generator=g)
+    kb[..., 0] = torch.arange(7.0)[:, None, None] * (4.0 if rising else 0.0)
+    kb, vb = kb.to(dtype), (1 + torch.rand(7, Hkv, BLOCK, d, generator=g)).to(dtype)
+    q = torch.randn(B * n, Hq, d, generator=g)
+    q[..., 0] = math.sqrt(d) / 2
+    q = q.to(dtype)
+    table = torch.randint(0, 7, (nb,), generator=g, dtype=torch.int32)
+    if rising:
+        table = table.sort().values
+    desc = v.kv_desc(Hq, Hkv, d, dtype=dtype)
+    ws = v.kv_workspace(desc)
+    kw = dict(q=q.cuda(), k_cache=kb.cuda(), v_cache=vb.cuda(), ws=ws,
+              q_start=torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda"),
+              kv_len=torch.full((B,), L, device="cuda"), block_table=table.expand(B, nb).contiguous().cuda())
+    got = []
+    for sparse in (False, True):
+        out = torch.full((B * n, Hq, d), 7.0, dtype=dtype, device="cuda")
+        lse = torch.full((B * n, Hq), 7.0, device="cuda")
+        if sparse:
+            v.block_sparse_attention(desc, idx=None, n_local=nb, out=out, lse=lse, **kw)
+        else:
+            v.paged_attention(desc, out=out, lse=lse, **kw)
+        assert v.device_status(ws) == 0
+        got.append((out.double().cpu(), lse.double().cpu()))
+    kd, vd, gr = kb.double(), vb.double(), Hq // Hkv
+    for t in {0, B * n - 1, *range(3, B * n, max(1, B * n // 9))}:
+        p = L - n + t % n
+        last = p // BLOCK
+        # how often the query sees each of the 7 x 128 keys
+        often = torch.bincount(table[:last], minlength=7).double()[:, None].repeat(1, BLOCK)
+        often[table[last], :p % BLOCK + 1] += 1
+        for h in range(Hkv):
+            hs = slice(h * gr, h * gr + gr)
+            qq, k, x = q[t, hs].double(), kd[:, h].flatten(0, 1), vd[:, h].flatten(0, 1)
+            s = qq @ k.T / math.sqrt(d) + often.flatten().log()
+            e = d * 2.0 ** -23 * (qq.abs() @ k.abs().T).amax(1)[:, None] / math.sqrt(d) + 2.0 ** -18
+            z = s.logsumexp(1)
+            want = (s - z[:, None]).exp() @ x
+            tol = u * want + (u + 2 * e + 2.0 ** -12) * want * (1 + u)
+            for out, lse in got:
+                assert ((out[t, hs] - want).abs() <= tol).all(), (t, h)
+                assert ((lse[t, hs] - z).abs() <= e[:, 0] + 2.0 ** -20 * (1 + z.abs())).all(), (t, h)
